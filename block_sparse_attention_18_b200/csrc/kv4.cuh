@@ -1,0 +1,94 @@
+// Device helpers of the paged 4-bit key/value cache (format: sparstar.h).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "sparstar.h"
+#include "sparstar_internal.h"
+
+namespace sparstar {
+
+constexpr float kKv4Limit = 26880.0f;  // 7 * the largest scale, 3840
+constexpr int kScaleExp = 107;         // bf16 exponent field of scale codes 0..7: 2^-20
+
+// Scale code -> scale: four significant bits, so bf16 and fp32 hold it.
+__device__ __forceinline__ float kv4_scale(uint32_t code) {
+    return __uint_as_float((code + (kScaleExp << 3)) << 20);
+}
+// Two scale codes in the low bytes of the halves of x -> a bf16 pair.
+__device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t x) {
+    return (x << 4) + ((uint32_t)kScaleExp << 7) * 0x10001u;
+}
+
+// Codes 2i and 2i + 1 of a word as the bf16 pair 128 + code (bf16 holds the
+// integers up to 256, so the code goes straight into the mantissa).
+__device__ __forceinline__ uint32_t kv4_pair128(uint32_t w, int i) {
+    return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+}
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) {
+    return *reinterpret_cast<__nv_bfloat162 *>(&x);
+}
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) {
+    return *reinterpret_cast<uint32_t *>(&x);
+}
+// s * (code - 8) for two codes, as (128 + code) * s - 136 * s.  Exact: 136 s
+// has at most 8 significant bits (17 * m for m = 8..15 is below 256), the
+// fma rounds once, and its result (7 or fewer bits) needs no rounding.
+__device__ __forceinline__ uint32_t kv4_dequant(uint32_t pair128, uint32_t s, uint32_t minus136s) {
+    return as_u32(__hfma2(as_bf162(pair128), as_bf162(s), as_bf162(minus136s)));
+}
+__device__ __forceinline__ uint32_t kv4_minus136(uint32_t s) {
+    return as_u32(__hmul2(as_bf162(s), __float2bfloat162_rn(-136.0f)));
+}
+
+// Element e of a word: its nibble.
+__host__ __device__ constexpr int kv4_nibble(int e) { return (e & 1) * 4 + (e >> 1); }
+
+// Transposes the 8 x 8 nibbles of eight words held by nibble position: word
+// p, nibble r goes to word r, nibble p.  Words are given by element (token
+// or channel) e at index e; positions follow from kv4_nibble on both sides.
+__device__ __forceinline__ void kv4_transpose(uint32_t (&w)[8]) {
+    uint32_t r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[kv4_nibble(e)] = w[e];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {  // 16-bit halves of rows p and p + 4
+        const uint32_t a = r[p], b = r[p + 4];
+        r[p] = __byte_perm(a, b, 0x5410);
+        r[p + 4] = __byte_perm(a, b, 0x7632);
+    }
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {  // bytes of rows p and p + 2
+        if (p & 2) continue;
+        const uint32_t a = r[p], b = r[p + 2];
+        r[p] = __byte_perm(a, b, 0x6240);
+        r[p + 2] = __byte_perm(a, b, 0x7351);
+    }
+#pragma unroll
+    for (int p = 0; p < 8; p += 2) {  // nibbles of rows p and p + 1
+        const uint32_t a = r[p], b = r[p + 1];
+        r[p] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+        r[p + 1] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = r[kv4_nibble(e)];
+}
+
+__device__ __forceinline__ void kv4_flag(int32_t *status, int32_t bits) {
+    if (status) atomicOr(status, bits);
+}
+
+// Slot of list entry i; -1 when outside the cache.
+__device__ __forceinline__ int kv4_slot(const Kv4 &c, const int32_t *seqs, int i) {
+    const int s = seqs ? __ldg(seqs + i) : i;
+    return s >= 0 && s < c.n_seqs ? s : -1;
+}
+// Tokens of a slot, whatever the memory holds: 0 .. 128 max_pages.
+__device__ __forceinline__ int kv4_len(const Kv4 &c, int slot) {
+    const int L = c.lens[slot];
+    const int most = c.max_pages * kBlock;
+    return L < 0 ? 0 : (L > most ? most : L);
+}
+
+}  // namespace sparstar

@@ -67,8 +67,9 @@ SPARSTAR_API const char *sparstar_strerror(int code) {
     case SPARSTAR_ECUDA: return "CUDA runtime error";
     case SPARSTAR_ESIZE:
         return "size limit: max_sel below the selected count, the intermediates exceed the "
-               "static arena (SPARSTAR_STATIC_ARENA_BYTES), or nKB above "
-               "sparstar_score_select_max_nkb(D)";
+               "static arena (SPARSTAR_STATIC_ARENA_BYTES), nKB above "
+               "sparstar_score_select_max_nkb(D), or work_bytes below "
+               "sparstar_kv4_attn_work_bytes";
     case SPARSTAR_ENODEV: return "no sm_100 device available for this call";
     default: return "unknown status";
     }
@@ -344,6 +345,162 @@ SPARSTAR_API int sparstar_transfer_lists(const int32_t *src_idx, const int32_t *
     return cuda_status(sparstar::launch_transfer_lists(src_idx, src_cnt, src_max_sel, B * H, ly,
                                                        dst_idx, dst_cnt, dst_max_sel,
                                                        static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks of the cache that every call shares; fills the kernels' view.
+int kv4_cache_check(const sparstar_kv4_cache *cache, bool uses_work, sparstar::Kv4 *c) {
+    if (!cache || !cache->pages || !cache->refs || !cache->table || !cache->lens ||
+        !head_dim_ok(cache->D))
+        return SPARSTAR_EINVAL;
+    if (uses_work && !cache->work) return SPARSTAR_EINVAL;
+    if (!aligned16(cache->pages) || !aligned16(cache->refs) || !aligned4(cache->table) ||
+        !aligned4(cache->lens) || !aligned4(cache->work))
+        return SPARSTAR_EINVAL;
+    // Positions are 32-bit; work indexes three lists of n_pages.
+    if (cache->n_pages < 1 || cache->n_pages > (1 << 28) || cache->n_seqs < 1 ||
+        cache->n_seqs > (1 << 20) || cache->max_pages < 1 || cache->max_pages > (1 << 23) ||
+        cache->Hkv < 1 || cache->Hkv > 65535)
+        return SPARSTAR_EINVAL;
+    *c = sparstar::Kv4{static_cast<uint8_t *>(cache->pages), cache->refs,
+                       cache->table,  cache->lens,
+                       cache->work,   (int32_t)cache->n_pages,
+                       (int32_t)cache->n_seqs, (int32_t)cache->max_pages,
+                       (int32_t)cache->Hkv,    (int32_t)cache->D};
+    return SPARSTAR_OK;
+}
+
+int kv4_token_check(int64_t n, int64_t T, const sparstar::Kv4 &c, const void *k, const void *v,
+                    const void *starts, const void *counts) {
+    if (n < 1 || n > c.n_seqs || T < 1 || T > kMaxTokens) return SPARSTAR_EINVAL;
+    if (!aligned16(k) || !aligned16(v) || !aligned4(starts) || !aligned4(counts))
+        return SPARSTAR_EINVAL;
+    // one CTA a touched page of every sequence and head
+    if (n * (ceil_div(T, kBlock) + 1) > kMaxGrid / c.Hkv) return SPARSTAR_EINVAL;
+    return SPARSTAR_OK;
+}
+
+}  // namespace
+
+SPARSTAR_API int64_t sparstar_kv4_page_bytes(int64_t D) {
+    return head_dim_ok(D) ? sparstar::kv4_page_bytes((int)D) : -1;
+}
+
+SPARSTAR_API int64_t sparstar_kv4_work_ints(int64_t n_pages, int64_t n_seqs) {
+    if (n_pages < 1 || n_seqs < 1 || n_pages > (1 << 28) || n_seqs > (1 << 20)) return -1;
+    return sparstar::kv4_work_ints(n_pages, n_seqs);
+}
+
+SPARSTAR_API int sparstar_kv4_resize(const sparstar_kv4_cache *cache, const int32_t *seqs,
+                                     const int32_t *new_lens, int64_t n, int32_t *status,
+                                     void *stream) {
+    TraceRange trace("sparstar_kv4_resize");
+    sparstar::Kv4 c;
+    if (int rc = kv4_cache_check(cache, true, &c)) return rc;
+    if (!new_lens || n < 1 || n > c.n_seqs || !aligned4(seqs) || !aligned4(new_lens))
+        return SPARSTAR_EINVAL;
+    if (int rc = device_check()) return rc;
+    return cuda_status(sparstar::launch_kv4_resize(c, seqs, new_lens, (int)n, status,
+                                                   static_cast<cudaStream_t>(stream)));
+}
+
+SPARSTAR_API int sparstar_kv4_fork(const sparstar_kv4_cache *cache, const int32_t *src,
+                                   const int32_t *dst, const int32_t *len, int64_t n, int deep,
+                                   int32_t *status, void *stream) {
+    TraceRange trace("sparstar_kv4_fork");
+    sparstar::Kv4 c;
+    if (int rc = kv4_cache_check(cache, true, &c)) return rc;
+    if (!src || !dst || n < 1 || n > c.n_seqs || (deep != 0 && deep != 1) || !aligned4(src) ||
+        !aligned4(dst) || !aligned4(len))
+        return SPARSTAR_EINVAL;
+    if (int rc = device_check()) return rc;
+    return cuda_status(sparstar::launch_kv4_fork(c, src, dst, len, (int)n, deep != 0, status,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+SPARSTAR_API int sparstar_kv4_compact(const sparstar_kv4_cache *cache, int32_t *n_live,
+                                      void *stream) {
+    TraceRange trace("sparstar_kv4_compact");
+    sparstar::Kv4 c;
+    if (int rc = kv4_cache_check(cache, true, &c)) return rc;
+    if (!n_live || !aligned4(n_live)) return SPARSTAR_EINVAL;
+    if (int rc = device_check()) return rc;
+    return cuda_status(
+        sparstar::launch_kv4_compact(c, n_live, static_cast<cudaStream_t>(stream)));
+}
+
+SPARSTAR_API int sparstar_kv4_write(const sparstar_kv4_cache *cache, const void *k,
+                                    const void *v, int dtype, int64_t n, int64_t T,
+                                    const int32_t *seqs, const int32_t *starts,
+                                    const int32_t *counts, int32_t *status, void *stream) {
+    TraceRange trace("sparstar_kv4_write");
+    sparstar::Kv4 c;
+    if (!dtype_ok(dtype)) return SPARSTAR_EDTYPE;
+    if (int rc = kv4_cache_check(cache, false, &c)) return rc;
+    if (!k || !v) return SPARSTAR_EINVAL;
+    if (int rc = kv4_token_check(n, T, c, k, v, starts, counts)) return rc;
+    if (int rc = device_check()) return rc;
+    return cuda_status(sparstar::launch_kv4_write(c, k, v, dtype, (int)n, T, seqs, starts,
+                                                  counts, status,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+SPARSTAR_API int sparstar_kv4_read(const sparstar_kv4_cache *cache, void *k, void *v, int dtype,
+                                   int64_t n, int64_t T, const int32_t *seqs,
+                                   const int32_t *starts, const int32_t *counts,
+                                   int32_t *status, void *stream) {
+    TraceRange trace("sparstar_kv4_read");
+    sparstar::Kv4 c;
+    if (!dtype_ok(dtype)) return SPARSTAR_EDTYPE;
+    if (int rc = kv4_cache_check(cache, false, &c)) return rc;
+    if (!k && !v) return SPARSTAR_EINVAL;
+    if (int rc = kv4_token_check(n, T, c, k, v, starts, counts)) return rc;
+    if (int rc = device_check()) return rc;
+    return cuda_status(sparstar::launch_kv4_read(c, k, v, dtype, (int)n, T, seqs, starts, counts,
+                                                 status, static_cast<cudaStream_t>(stream)));
+}
+
+SPARSTAR_API int64_t sparstar_kv4_attn_work_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq,
+                                                  int64_t D, int dtype) {
+    if (n < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq > 65535 || Lq < 1 || Lq > kMaxTokens ||
+        !head_dim_ok(D) || !dtype_ok(dtype) || n > kMaxGrid / Hq || n * Hq > kMaxGrid / Lq)
+        return -1;
+    return sparstar::kv4_attn_work_bytes(n, Hq, Hkv, Lq, (int)D, dtype);
+}
+
+SPARSTAR_API int sparstar_kv4_attn(const sparstar_kv4_cache *cache, const void *q, int dtype,
+                                   int64_t n, int64_t Hq, int64_t Lq, const int32_t *seqs,
+                                   float tau, int causal, const int32_t *kv_idx,
+                                   const int32_t *kv_cnt, int64_t max_sel, void *out, float *lse,
+                                   void *work, int64_t work_bytes, int32_t *status,
+                                   void *stream) {
+    TraceRange trace("sparstar_kv4_attn");
+    sparstar::Kv4 c;
+    if (!dtype_ok(dtype)) return SPARSTAR_EDTYPE;
+    if (int rc = kv4_cache_check(cache, false, &c)) return rc;
+    if (!q || !out || (causal != 0 && causal != 1) || !std::isfinite(tau))
+        return SPARSTAR_EINVAL;
+    // lists: both or none
+    if (max_sel < 0 || max_sel > 0x7fffffffLL || (max_sel > 0 && (!kv_idx || !kv_cnt)) ||
+        (kv_idx && !kv_cnt))
+        return SPARSTAR_EINVAL;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(work) || !aligned4(seqs) ||
+        !aligned4(kv_idx) || !aligned4(kv_cnt) || !aligned4(lse))
+        return SPARSTAR_EINVAL;
+    // One list entry names one of n_seqs slots, or several entries the same.
+    const int64_t need = sparstar_kv4_attn_work_bytes(n, Hq, c.Hkv, Lq, c.D, dtype);
+    if (need < 0 || (!seqs && n > c.n_seqs)) return SPARSTAR_EINVAL;
+    if (work_bytes < need) return SPARSTAR_ESIZE;
+    if (need > 0 && !work) return SPARSTAR_EINVAL;
+    if (int rc = device_check()) return rc;
+    const sparstar::Kv4Attn a{q,      (int32_t)n, (int32_t)Hq,      (int32_t)Lq, causal, seqs,
+                              tau,    kv_idx,     kv_cnt,           (int32_t)max_sel,
+                              out,    lse,        work,             status};
+    return cuda_status(
+        sparstar::launch_kv4_attn(c, a, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 SPARSTAR_API int sparstar_test_attn_timeout(const void *q, const void *k, const void *v,

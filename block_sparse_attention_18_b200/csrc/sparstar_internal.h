@@ -83,4 +83,48 @@ cudaError_t launch_transfer_lists(const int32_t *src_idx, const int32_t *src_cnt
 int64_t transfer_max_nkb();
 int64_t transfer_max_sel(const TransferLayout &ly, int64_t src_max_sel);  // host
 
+// The paged 4-bit key/value cache, as the kernels see it (arguments checked).
+struct Kv4 {
+    uint8_t *pages;
+    int32_t *refs, *table, *lens, *work;
+    int32_t n_pages, n_seqs, max_pages, Hkv, D;
+};
+constexpr int kGroup = 32;  // channels of one token and head that share a scale
+// One page of one head: key codes, key scales, value codes, value scales.
+__host__ __device__ constexpr int kv4_code_bytes(int D) { return kBlock * D / 2; }
+__host__ __device__ constexpr int kv4_scale_bytes(int D) { return kBlock * D / kGroup; }
+__host__ __device__ constexpr int kv4_half_bytes(int D) {
+    return kv4_code_bytes(D) + kv4_scale_bytes(D);
+}
+__host__ __device__ constexpr int kv4_page_bytes(int D) { return 2 * kv4_half_bytes(D); }
+int64_t kv4_work_ints(int64_t n_pages, int64_t n_seqs);
+
+cudaError_t launch_kv4_resize(const Kv4 &c, const int32_t *seqs, const int32_t *new_lens, int n,
+                              int32_t *status, cudaStream_t stream);
+cudaError_t launch_kv4_fork(const Kv4 &c, const int32_t *src, const int32_t *dst,
+                            const int32_t *len, int n, bool deep, int32_t *status,
+                            cudaStream_t stream);
+cudaError_t launch_kv4_compact(const Kv4 &c, int32_t *n_live, cudaStream_t stream);
+cudaError_t launch_kv4_write(const Kv4 &c, const void *k, const void *v, int dtype, int n,
+                             int64_t T, const int32_t *seqs, const int32_t *starts,
+                             const int32_t *counts, int32_t *status, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4 &c, void *k, void *v, int dtype, int n, int64_t T,
+                            const int32_t *seqs, const int32_t *starts, const int32_t *counts,
+                            int32_t *status, cudaStream_t stream);
+// One attention call over the cache.
+struct Kv4Attn {
+    const void *q;
+    int32_t n, Hq, Lq, causal;
+    const int32_t *seqs;
+    float tau;
+    const int32_t *kv_idx, *kv_cnt;
+    int32_t max_sel;
+    void *out;
+    float *lse;
+    void *work;
+    int32_t *status;
+};
+cudaError_t launch_kv4_attn(const Kv4 &c, const Kv4Attn &a, int dtype, cudaStream_t stream);
+int64_t kv4_attn_work_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq, int D, int dtype);
+
 }  // namespace sparstar

@@ -19,8 +19,16 @@ BLOCK = 128
 OK, EINVAL, EDTYPE, ECUDA, ESIZE, ENODEV = range(6)
 STATUS_BAD_INDEX = 0x1
 STATUS_TIMEOUT = 0x2
+STATUS_NO_PAGES = 0x4
+STATUS_CLAMPED = 0x8
+STATUS_SHARED = 0x10
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+class _Kv4Struct(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("pages", "refs", "table", "lens", "work")] + \
+               [(name, ctypes.c_int64) for name in ("n_pages", "n_seqs", "max_pages", "Hkv", "D")]
 
 
 def _load():
@@ -62,6 +70,23 @@ def _load():
     L.sparstar_strerror.argtypes = [i32]
     L.sparstar_strerror.restype = ctypes.c_char_p
     L.sparstar_version.restype = i32
+    kv4 = ctypes.POINTER(_Kv4Struct)
+    L.sparstar_kv4_page_bytes.argtypes = [i64]
+    L.sparstar_kv4_page_bytes.restype = i64
+    L.sparstar_kv4_work_ints.argtypes = [i64, i64]
+    L.sparstar_kv4_work_ints.restype = i64
+    L.sparstar_kv4_resize.argtypes = [kv4, vp, vp, i64, vp, vp]
+    L.sparstar_kv4_fork.argtypes = [kv4, vp, vp, vp, i64, i32, vp, vp]
+    L.sparstar_kv4_compact.argtypes = [kv4, vp, vp]
+    L.sparstar_kv4_write.argtypes = [kv4, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp]
+    L.sparstar_kv4_read.argtypes = [kv4, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp]
+    L.sparstar_kv4_attn.argtypes = [kv4, vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, i64, vp,
+                                    vp, vp, i64, vp, vp]
+    L.sparstar_kv4_attn_work_bytes.argtypes = [i64, i64, i64, i64, i64, i32]
+    L.sparstar_kv4_attn_work_bytes.restype = i64
+    for name in ("sparstar_kv4_resize", "sparstar_kv4_fork", "sparstar_kv4_compact",
+                 "sparstar_kv4_write", "sparstar_kv4_read", "sparstar_kv4_attn"):
+        getattr(L, name).restype = i32
     for name in ("sparstar_block_pool", "sparstar_block_score", "sparstar_select",
                  "sparstar_attn_fwd", "sparstar_forward", "sparstar_block_pool_qk",
                  "sparstar_score_select", "sparstar_forward_fused", "sparstar_retained_mass",
@@ -110,6 +135,9 @@ def nblocks(L: int) -> int:
 
 def default_tau(D: int) -> float:
     return float(torch.tensor(1.0 / math.sqrt(D), dtype=torch.float32))
+
+
+_TAU = {D: default_tau(D) for D in (64, 128)}
 
 
 def sparstar_forced_blocks(text_len: int, image_ref_len: int) -> int:
@@ -392,6 +420,243 @@ def sparstar_transfer_lists(kv_idx, kv_cnt, src_len, dst_len, dst_idx=None, dst_
                                        _ptr(dst_idx), _ptr(dst_cnt), dst_idx.shape[-1],
                                        _stream(stream)), "sparstar_transfer_lists")
     return dst_idx, dst_cnt
+
+
+def sparstar_kv4_page_bytes(D: int) -> int:
+    return lib.sparstar_kv4_page_bytes(D)
+
+
+class Kv4Cache:
+    """Caller-owned device buffers of a paged 4-bit key/value cache.
+
+    ``Kv4Cache.empty(...)`` allocates an empty one; the constructor takes
+    buffers that the caller has: pages [n_pages, Hkv, page_bytes(D)] uint8,
+    refs [n_pages], table [n_seqs, max_pages] and lens [n_seqs] int32, and
+    the scratch ``work`` of the page calls (allocated when not given).
+    """
+
+    def __init__(self, pages, refs, table, lens, D: int, work=None):
+        _dev(pages, "pages", torch.uint8)
+        for t, name in ((refs, "refs"), (table, "table"), (lens, "lens")):
+            _dev(t, name, torch.int32)
+            if t.device != pages.device:
+                raise ValueError("%s must be on %s, got %s" % (name, pages.device, t.device))
+        n_pages, n_seqs = refs.numel(), lens.numel()
+        if pages.dim() != 3 or pages.shape[0] != n_pages \
+                or pages.shape[2] != sparstar_kv4_page_bytes(D):
+            raise ValueError("pages must be [n_pages, Hkv, page_bytes(D)], got %s"
+                             % (tuple(pages.shape),))
+        if refs.dim() != 1 or lens.dim() != 1 or table.dim() != 2 or table.shape[0] != n_seqs:
+            raise ValueError("refs must be [n_pages], lens [n_seqs] and table [n_seqs, max_pages]")
+        ints = lib.sparstar_kv4_work_ints(n_pages, n_seqs)
+        if ints < 0:
+            raise SparstarError(EINVAL, "Kv4Cache")
+        if work is None:
+            work = torch.empty(ints, device=pages.device, dtype=torch.int32)
+        _dev(work, "work", torch.int32)
+        if work.numel() < ints or work.device != pages.device:
+            raise ValueError("work must hold %d int32 on %s" % (ints, pages.device))
+        self.pages, self.refs, self.table, self.lens, self.work = pages, refs, table, lens, work
+        self.n_pages, self.n_seqs, self.max_pages = n_pages, n_seqs, table.shape[1]
+        self.Hkv, self.D, self.device = pages.shape[1], D, pages.device
+        self._struct = _Kv4Struct(pages.data_ptr(), refs.data_ptr(), table.data_ptr(),
+                                  lens.data_ptr(), work.data_ptr(), n_pages, n_seqs,
+                                  table.shape[1], pages.shape[1], D)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_seqs: int, max_pages: int, Hkv: int, D: int, device="cuda"):
+        i32 = dict(device=device, dtype=torch.int32)
+        per_head = sparstar_kv4_page_bytes(D)
+        if per_head < 0 or min(n_pages, n_seqs, max_pages, Hkv) < 1:
+            raise SparstarError(EINVAL, "Kv4Cache.empty")
+        return cls(torch.empty(n_pages, Hkv, per_head, device=device, dtype=torch.uint8),
+                   torch.zeros(n_pages, **i32), torch.full((n_seqs, max_pages), -1, **i32),
+                   torch.zeros(n_seqs, **i32), D)
+
+
+def _kv4_ints(cache, t, name, n=None):
+    """A device list of int32 (or None): its pointer."""
+    if t is None:
+        return None
+    _dev(t, name, torch.int32)
+    if t.device != cache.device or t.dim() != 1 or (n is not None and t.numel() != n):
+        raise ValueError("%s must be int32 [%s] on %s" % (name, "n" if n is None else n,
+                                                          cache.device))
+    return t.data_ptr()
+
+
+def _kv4_tensor(cache, t, name, dtype, shape):
+    _dev(t, name, dtype)
+    if t.device != cache.device or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s on %s, got %s on %s"
+                         % (name, tuple(shape), cache.device, tuple(t.shape), t.device))
+    return t.data_ptr()
+
+
+def _kv4_status(cache, status):
+    return None if status is None else _kv4_tensor(cache, status, "status", torch.int32, (1,))
+
+
+class _Kv4Call:
+    """The device of the cache and the stream of a call, as context."""
+
+    def __init__(self, cache, stream):
+        self.guard = None
+        if torch.cuda.current_device() != cache.device.index:
+            self.guard = torch.cuda.device(cache.device)
+        self.given = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        s = self.given if self.given is not None else torch.cuda.current_stream()
+        return s
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def sparstar_kv4_resize(cache: Kv4Cache, new_lens, seqs=None, status=None, stream=None):
+    """Sets the lengths of n sequences (0 frees one); takes and gives pages."""
+    n = new_lens.numel()
+    with _Kv4Call(cache, stream) as s:
+        _check(lib.sparstar_kv4_resize(cache._struct, _kv4_ints(cache, seqs, "seqs", n),
+                                       _kv4_ints(cache, new_lens, "new_lens"), n,
+                                       _kv4_status(cache, status), s.cuda_stream),
+               "sparstar_kv4_resize")
+
+
+def sparstar_kv4_fork(cache: Kv4Cache, src, dst, lens=None, deep: bool = False, status=None,
+                      stream=None):
+    """Empty sequences dst take the tokens of src: shared pages, or (deep) copies."""
+    n = src.numel()
+    with _Kv4Call(cache, stream) as s:
+        _check(lib.sparstar_kv4_fork(cache._struct, _kv4_ints(cache, src, "src"),
+                                     _kv4_ints(cache, dst, "dst", n),
+                                     _kv4_ints(cache, lens, "lens", n), n, int(bool(deep)),
+                                     _kv4_status(cache, status), s.cuda_stream),
+               "sparstar_kv4_fork")
+
+
+def sparstar_kv4_compact(cache: Kv4Cache, n_live=None, stream=None):
+    """Moves the live pages to the lowest places; returns their number (device)."""
+    with _Kv4Call(cache, stream) as s:
+        if n_live is None:
+            n_live = _kv4_new(s, (1,), torch.int32, cache.device)
+        _check(lib.sparstar_kv4_compact(cache._struct,
+                                        _kv4_tensor(cache, n_live, "n_live", torch.int32, (1,)),
+                                        s.cuda_stream), "sparstar_kv4_compact")
+    return n_live
+
+
+def _kv4_new(stream, shape, dtype, device):
+    """A tensor of the stream that the call runs on."""
+    if stream == torch.cuda.current_stream():
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def sparstar_kv4_write(cache: Kv4Cache, k, v, seqs=None, starts=None, counts=None, status=None,
+                       stream=None):
+    """Stores k, v [n, Hkv, T, D] at positions starts (default: the last T)."""
+    if k.dim() != 4:
+        raise ValueError("k must be [n, Hkv, T, D]")
+    n, _, T, _ = k.shape
+    shape = (n, cache.Hkv, T, cache.D)
+    with _Kv4Call(cache, stream) as s:
+        _check(lib.sparstar_kv4_write(cache._struct, _kv4_tensor(cache, k, "k", None, shape),
+                                      _kv4_tensor(cache, v, "v", k.dtype, shape),
+                                      _DTYPE.get(k.dtype, -1), n, T,
+                                      _kv4_ints(cache, seqs, "seqs", n),
+                                      _kv4_ints(cache, starts, "starts", n),
+                                      _kv4_ints(cache, counts, "counts", n),
+                                      _kv4_status(cache, status), s.cuda_stream),
+               "sparstar_kv4_write")
+
+
+def sparstar_kv4_read(cache: Kv4Cache, T: int, n: int = None, dtype=torch.bfloat16, seqs=None,
+                      starts=None, counts=None, k=None, v=None, status=None, stream=None):
+    """The values of T tokens of each of n sequences; returns (k, v)
+    [n, Hkv, T, D].  Rows beyond counts are not written (buffers that the
+    call allocates hold zeros there).  n, unless given, follows from seqs,
+    starts, counts, k or v, and is every sequence without them."""
+    if n is None:
+        sizes = [t.shape[0] for t in (seqs, starts, counts, k, v) if t is not None]
+        n = sizes[0] if sizes else cache.n_seqs
+    shape = (n, cache.Hkv, T, cache.D)
+    if k is not None or v is not None:
+        dtype = (k if k is not None else v).dtype
+    with _Kv4Call(cache, stream) as s:
+        if k is None and v is None:
+            k, v = (_kv4_new(s, shape, dtype, cache.device) for _ in range(2))
+            if counts is not None:
+                with torch.cuda.stream(s):
+                    k.zero_(), v.zero_()
+        kp = None if k is None else _kv4_tensor(cache, k, "k", dtype, shape)
+        vp = None if v is None else _kv4_tensor(cache, v, "v", dtype, shape)
+        _check(lib.sparstar_kv4_read(cache._struct, kp, vp, _DTYPE.get(dtype, -1), n, T,
+                                     _kv4_ints(cache, seqs, "seqs", n),
+                                     _kv4_ints(cache, starts, "starts", n),
+                                     _kv4_ints(cache, counts, "counts", n),
+                                     _kv4_status(cache, status), s.cuda_stream),
+               "sparstar_kv4_read")
+    return k, v
+
+
+def sparstar_kv4_attn_work_bytes(n: int, Hq: int, Hkv: int, Lq: int, D: int,
+                                 dtype=torch.bfloat16) -> int:
+    return lib.sparstar_kv4_attn_work_bytes(n, Hq, Hkv, Lq, D, _DTYPE.get(dtype, -1))
+
+
+def sparstar_kv4_attn(cache: Kv4Cache, q, seqs=None, tau: float = None, causal: bool = False,
+                      kv_idx=None, kv_cnt=None, out=None, lse=None, want_lse: bool = True,
+                      work=None, status=None, stream=None):
+    """Attention of q [n, Hq, Lq, D] over the cached tokens of n sequences;
+    returns (out, lse).  ``work`` (uint8) is allocated when not given."""
+    if q.dim() != 4:
+        raise ValueError("q must be [n, Hq, Lq, D]")
+    n, Hq, Lq, D = q.shape
+    dt = _DTYPE.get(q.dtype, -1)
+    if D != cache.D:
+        raise ValueError("q has head dim %d, the cache %d" % (D, cache.D))
+    if tau is None:
+        tau = _TAU[D]
+    qp = _kv4_tensor(cache, q, "q", None, q.shape)
+    if (kv_idx is None) != (kv_cnt is None):
+        raise ValueError("kv_idx and kv_cnt go together")
+    max_sel = 0
+    if kv_idx is not None:
+        rows = (n, Hq, nblocks(Lq))
+        max_sel = kv_idx.shape[-1]
+        ip = _kv4_tensor(cache, kv_idx, "kv_idx", torch.int32, rows + (max_sel,))
+        cp = _kv4_tensor(cache, kv_cnt, "kv_cnt", torch.int32, rows)
+    else:
+        ip = cp = None
+    need = lib.sparstar_kv4_attn_work_bytes(n, Hq, cache.Hkv, Lq, D, dt)
+    if need < 0:
+        raise SparstarError(EDTYPE if dt < 0 else EINVAL, "sparstar_kv4_attn")
+    with _Kv4Call(cache, stream) as s:
+        if out is None:
+            out = _kv4_new(s, q.shape, q.dtype, cache.device)
+        if lse is None and want_lse:
+            lse = _kv4_new(s, (n, Hq, Lq), torch.float32, cache.device)
+        if work is None and need:
+            work = _kv4_new(s, (need,), torch.uint8, cache.device)
+        elif work is not None:
+            _dev(work, "work", torch.uint8)
+            if work.device != cache.device:
+                raise ValueError("work must be on %s" % cache.device)
+        _check(lib.sparstar_kv4_attn(
+            cache._struct, qp, dt, n, Hq, Lq, _kv4_ints(cache, seqs, "seqs", n), tau,
+            int(bool(causal)), ip, cp, max_sel,
+            _kv4_tensor(cache, out, "out", q.dtype, q.shape),
+            None if lse is None else _kv4_tensor(cache, lse, "lse", torch.float32, (n, Hq, Lq)),
+            None if work is None else work.data_ptr(), 0 if work is None else work.numel(),
+            _kv4_status(cache, status), s.cuda_stream), "sparstar_kv4_attn")
+    return out, lse
 
 
 def sparstar_test_attn_timeout(q, k, v, kv_idx, kv_cnt, out, status, stream=None):

@@ -69,13 +69,17 @@ enum sparstar_status {
     SPARSTAR_EINVAL = 1,  /* bad size, null pointer, misalignment, density outside (0,1] */
     SPARSTAR_EDTYPE = 2,  /* unknown dtype code */
     SPARSTAR_ECUDA = 3,   /* a CUDA runtime call or launch failed */
-    SPARSTAR_ESIZE = 4,   /* max_sel < selected count, or a call too big for the static arena */
+    SPARSTAR_ESIZE = 4,   /* max_sel < selected count, a call too big for the static arena, or
+                             work_bytes below sparstar_kv4_attn_work_bytes */
     SPARSTAR_ENODEV = 5   /* no usable sm_100 device for this call */
 };
 
-/* Bits the attention kernels OR into *status (when status is non-NULL). */
+/* Bits the kernels OR into *status (when status is non-NULL). */
 #define SPARSTAR_STATUS_BAD_INDEX 0x1 /* a kv_idx entry outside [0, nKB) was skipped */
 #define SPARSTAR_STATUS_TIMEOUT 0x2   /* a pipeline wait gave up; output is invalid */
+#define SPARSTAR_STATUS_NO_PAGES 0x4  /* the 4-bit cache had too few free pages; see resize */
+#define SPARSTAR_STATUS_CLAMPED 0x8   /* a value beyond the 4-bit cache's range, or NaN, was stored */
+#define SPARSTAR_STATUS_SHARED 0x10   /* a write into a page that sequences share was left out */
 
 /*
  * sparstar_block_pool — step 1, block mean pooling.
@@ -373,6 +377,145 @@ int sparstar_transfer_lists(const int32_t *src_idx, const int32_t *src_cnt, int6
                             int64_t B, int64_t H, const int64_t *src_len, const int64_t *dst_len,
                             int32_t *dst_idx, int32_t *dst_cnt, int64_t dst_max_sel,
                             void *stream);
+
+/*
+ * Paged key/value cache in 4 bits.  The keys and values of the text, of the
+ * preceding clips and of finished scales are read again at every scale and
+ * clip that follows; these calls hold them in pages of 128 tokens (one key
+ * block of the block lists), 3.76 times smaller than bf16.
+ *
+ * Format.  A group is 32 consecutive channels of one token and head.  With a
+ * = the group's largest magnitude, its scale s is a / 7 rounded to four
+ * significant bits (nearest, ties to even) and kept in 8 bits:
+ * s = (1 + (c & 7) / 8) * 2^((c >> 3) - 20), c clamped to 0..255.  A channel
+ * x is held as the code round(x / s) + 8 (ties to even; codes 1..15; 0
+ * reads as -8 s).  It stands for s * (code - 8), which bf16 holds exactly.
+ * Magnitudes over 26880 (infinities too) are clamped to it and NaN is
+ * stored as 0; both set SPARSTAR_STATUS_CLAMPED.  Any bytes in a page read
+ * as finite values.
+ *
+ * A page of one head (sparstar_kv4_page_bytes(D) bytes) is
+ *   key codes    [128 tokens][D channels], key scales   [128][D / 32],
+ *   value codes  [D channels][128 tokens], value scales [D / 32][128].
+ * A 32-bit word holds eight consecutive codes e0..e7: its nibble i (0..3) is
+ * e[2i], nibble 4 + i is e[2i + 1].
+ *
+ * The cache is the caller's device memory, described by this struct (itself
+ * in host memory, read during the call only):
+ */
+typedef struct sparstar_kv4_cache {
+    void *pages;       /* [n_pages, Hkv, sparstar_kv4_page_bytes(D)], 16-byte aligned */
+    int32_t *refs;     /* [n_pages]: sequences that hold the page; 0 = free */
+    int32_t *table;    /* [n_seqs, max_pages]: page of tokens 128 j .. 128 j + 127; -1 = none */
+    int32_t *lens;     /* [n_seqs]: tokens held */
+    int32_t *work;     /* [sparstar_kv4_work_ints(n_pages, n_seqs)], scratch of the page calls */
+    int64_t n_pages, n_seqs, max_pages, Hkv, D;
+} sparstar_kv4_cache;
+/*
+ * An empty cache has refs and lens all 0 and table all -1; pages and work
+ * need no initial contents.  D is 64 or 128.  All calls on one cache that
+ * change it (and work) are ordered by the caller, on one stream or by events; calls that
+ * only read it (read, attn) may overlap each other.  Everything a call
+ * decides it decides on the device, from the tables at the time it runs, so
+ * every call can be captured into a CUDA graph.  Sequences are named by
+ * device lists `seqs` of n slots (NULL: slots 0..n-1; n <= n_seqs).  Entries
+ * that a call cannot serve (a slot outside the cache, the slot of an earlier
+ * entry of the same list where the call changes it, a length or range
+ * outside the sequence) are left out, and set SPARSTAR_STATUS_BAD_INDEX.
+ */
+
+/* Bytes of one page and head; -1 for a bad D. */
+int64_t sparstar_kv4_page_bytes(int64_t D);
+/* int32 elements of `work`; -1 for sizes below 1. */
+int64_t sparstar_kv4_work_ints(int64_t n_pages, int64_t n_seqs);
+
+/*
+ * sparstar_kv4_resize — sets the length of n sequences.
+ *   new_lens [n] int32 (device), 0 .. 128 max_pages; 0 frees the sequence
+ * Growing takes free pages, the lowest first, in the order of the list; when
+ * the last page is partial and shared, the sequence first gets its own copy
+ * of it.  If the free pages at the start of the call do not suffice for the
+ * entries up to and including one, that entry keeps its length and sets
+ * SPARSTAR_STATUS_NO_PAGES.  Shrinking gives pages up; they are free for the
+ * next call.  The new tokens are undefined until they are written.
+ */
+int sparstar_kv4_resize(const sparstar_kv4_cache *cache, const int32_t *seqs,
+                        const int32_t *new_lens, int64_t n, int32_t *status, void *stream);
+
+/*
+ * sparstar_kv4_fork — makes empty sequences dst[i] that hold the first
+ * len[i] tokens of src[i].
+ *   src, dst [n] int32 (device); len [n] int32 (device) or NULL (all of them)
+ *   deep     0: the pages are shared; 1: every page is copied
+ * An entry is left out (SPARSTAR_STATUS_BAD_INDEX) when dst[i] is not empty,
+ * repeats an earlier dst or when src[i] is any dst of the call.  Deep
+ * copies take pages as sparstar_kv4_resize does.
+ */
+int sparstar_kv4_fork(const sparstar_kv4_cache *cache, const int32_t *src, const int32_t *dst,
+                      const int32_t *len, int64_t n, int deep, int32_t *status, void *stream);
+
+/*
+ * sparstar_kv4_compact — moves pages so that the n live ones are pages
+ * 0..n-1, and writes n to *n_live (device).  The k-th lowest live page at or
+ * above n moves to the k-th lowest free page below n; pages behind the live
+ * ones keep their bytes.
+ */
+int sparstar_kv4_compact(const sparstar_kv4_cache *cache, int32_t *n_live, void *stream);
+
+/*
+ * sparstar_kv4_write — stores tokens (quantised) into pages a sequence has.
+ *   k, v   [n,Hkv,T,D] of `dtype` (device)
+ *   starts [n] int32 (device): position of token 0; NULL: the last tokens
+ *          of each sequence, lens - counts
+ *   counts [n] int32 (device): tokens to store, 0..T; NULL: T
+ * Tokens of pages that more than one sequence holds are left out
+ * (SPARSTAR_STATUS_SHARED).
+ */
+int sparstar_kv4_write(const sparstar_kv4_cache *cache, const void *k, const void *v, int dtype,
+                       int64_t n, int64_t T, const int32_t *seqs, const int32_t *starts,
+                       const int32_t *counts, int32_t *status, void *stream);
+
+/*
+ * sparstar_kv4_read — the values that tokens of the cache stand for.
+ *   k, v   [n,Hkv,T,D] of `dtype` (device, written; either may be NULL)
+ *   starts, counts as for write (starts NULL: position 0).  Rows at and
+ *          beyond counts[i] are left as they are.
+ */
+int sparstar_kv4_read(const sparstar_kv4_cache *cache, void *k, void *v, int dtype, int64_t n,
+                      int64_t T, const int32_t *seqs, const int32_t *starts,
+                      const int32_t *counts, int32_t *status, void *stream);
+
+/*
+ * sparstar_kv4_attn — forward attention of Lq query tokens a sequence over
+ * its cached keys and values.
+ *   q      [n,Hq,Lq,D] of `dtype` (device); Hq a multiple of Hkv; query head
+ *          h reads key head h / (Hq / Hkv)
+ *   seqs   as above; a slot may appear more than once
+ *   tau    softmax scale (normally D^-1/2)
+ *   causal 0: every token of the sequence is visible; 1: query token i of a
+ *          sequence of L tokens sees the tokens t <= L - Lq + i (the
+ *          queries are its last Lq tokens)
+ *   kv_idx [n,Hq,ceil(Lq/128),max_sel] and kv_cnt [n,Hq,ceil(Lq/128)] int32
+ *          (device): block lists as in sparstar_attn_fwd, a block being a
+ *          page of the sequence; both NULL (max_sel 0): every block
+ *   out    [n,Hq,Lq,D] of `dtype` (device, written)
+ *   lse    [n,Hq,Lq] fp32 (device, written), or NULL
+ *   work   device scratch of work_bytes >= sparstar_kv4_attn_work_bytes(...),
+ *          16-byte aligned, no initial contents; calls that may overlap on
+ *          the GPU need one each
+ * A row that sees no token gets out = 0 and lse = -inf; so do all rows of a
+ * slot outside the cache.  List entries outside the sequence's pages are
+ * skipped; both set SPARSTAR_STATUS_BAD_INDEX.
+ */
+int sparstar_kv4_attn(const sparstar_kv4_cache *cache, const void *q, int dtype, int64_t n,
+                      int64_t Hq, int64_t Lq, const int32_t *seqs, float tau, int causal,
+                      const int32_t *kv_idx, const int32_t *kv_cnt, int64_t max_sel, void *out,
+                      float *lse, void *work, int64_t work_bytes, int32_t *status,
+                      void *stream);
+
+/* Bytes of `work` (host only; 0 is possible); -1 for sizes that attn refuses. */
+int64_t sparstar_kv4_attn_work_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq, int64_t D,
+                                     int dtype);
 
 /*
  * sparstar_test_attn_timeout — TEST HOOK for failure detection, not part of
