@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libsparstar.so")
 
 SOURCES = ["sparstar_api.cu", "pool.cu", "score.cu", "select.cu", "score_select.cu",
            "attn_simt.cu", "attn_sm100.cu", "forward_static.cu", "mass.cu",
-           "transfer.cu", "kv4_pages.cu", "kv4_codec.cu", "kv4_attn.cu"]
+           "transfer.cu", "kv4_pages.cu", "kv4_codec.cu", "kv4_attn.cu",
+           "kv4_attn_few.cu"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",

@@ -125,6 +125,8 @@ struct Kv4Attn {
     int32_t *status;
 };
 cudaError_t launch_kv4_attn(const Kv4 &c, const Kv4Attn &a, int dtype, cudaStream_t stream);
+cudaError_t launch_kv4_attn_few(const Kv4 &c, const Kv4Attn &a, int dtype, cudaStream_t stream);
+int64_t kv4_attn_few_work_bytes(int D);
 int64_t kv4_attn_work_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq, int D, int dtype);
 
 }  // namespace sparstar
