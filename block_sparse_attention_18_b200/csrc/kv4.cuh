@@ -22,9 +22,19 @@ __device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t x) {
 }
 
 // Codes 2i and 2i + 1 of a word as the bf16 pair 128 + code (bf16 holds the
-// integers up to 256, so the code goes straight into the mantissa).
-__device__ __forceinline__ uint32_t kv4_pair128(uint32_t w, int i) {
-    return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+// integers up to 256, so the code goes straight into the mantissa).  `magic`
+// is kMagic in a register of the caller's (kv4_magic): the mask and the magic
+// then take one lop3, where two constants would take two.
+constexpr uint32_t kMagic = 0x43004300u;
+__device__ __forceinline__ uint32_t kv4_magic() {
+    uint32_t m = kMagic;
+    asm volatile("" : "+r"(m));
+    return m;
+}
+__device__ __forceinline__ uint32_t kv4_pair128(uint32_t w, int i, uint32_t magic) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(y) : "r"(w >> (4 * i)), "r"(magic));
+    return y;
 }
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) {
     return *reinterpret_cast<__nv_bfloat162 *>(&x);

@@ -37,10 +37,11 @@
 namespace sparstar {
 namespace {
 
-constexpr int kCtas = 148, kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kSlots = kCtas * kWarps;
+constexpr int kCtas = 148, kParts = 8;
+constexpr int kSlots = kCtas * kParts;
+constexpr int kArrivedBytes = SPARSTAR_KV4_WORK_ZEROS;  // kCtas words and alignment
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kMaxChunks = kThreads;
+constexpr int kChunks = 256;  // of sequences, for finding a place on the line
 
 struct Plan {
     int heads;       // query heads a key head
@@ -49,9 +50,11 @@ struct Plan {
     int nqb;         // query blocks of a head (lists)
     float sc;        // |tau| in log2 units
     uint32_t flip;   // sign bits to flip in q (tau < 0)
-    int32_t *head;   // [3][kSlots]: unit of the last and of the first partial result, and
-                     // of the last: 1 when it begins there and goes on, 2 when it ends there
-    float *records;  // [kSlots][2][R][D + 2]
+    uint32_t *arrived;  // [kCtas]: CTAs whose partial result of the unit that begins in this
+                        // CTA and goes on is stored; 0 between calls
+    float *joins;       // [kCtas][2][R][D + 2]: a CTA's partial results: of the unit that
+                        // goes on from the CTA before, of the one that begins here
+    float *ends;        // [kSlots][R][D + 2]: ends of units inside a part
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
@@ -61,6 +64,13 @@ __device__ __forceinline__ uint64_t globaltimer() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
+}
+__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -82,12 +92,14 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity) {
         if (__any_sync(0xffffffffu, globaltimer() - t0 > kTimeoutNs)) return false;
     }
 }
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_warp(uint64_t *mbar, uint32_t parity) {
+    const uint32_t bar = smem_u32(mbar);
     if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
     return wait_slow(bar, parity);
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
-                                          uint32_t bar) {
+                                          uint64_t *mbar) {
+    const uint32_t bar = smem_u32(mbar);
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
     asm volatile(
@@ -169,15 +181,15 @@ __device__ __forceinline__ int tiles_of(const Kv4 &c, const Kv4Attn &a, int i, i
 // The partition of the line: sequence i's units' tiles begin at
 // units * (tiles of the sequences before it).
 struct Line {
-    int64_t *prefix;  // shared: [kMaxChunks + 1] tiles before each chunk of sequences
+    int64_t *prefix;  // shared: [kChunks + 1] tiles before each chunk of sequences
     int chunk;        // sequences a chunk
 };
 __device__ int64_t build_line(const Kv4 &c, const Kv4Attn &a, Line &line, int64_t *shared,
                               int64_t *sums) {
     line.prefix = shared;
-    line.chunk = (a.n + kMaxChunks - 1) / kMaxChunks;
+    line.chunk = (a.n + kChunks - 1) / kChunks;
     int64_t mine = 0;
-    for (int k = 0; k < line.chunk; ++k) {
+    for (int k = 0; k < line.chunk && threadIdx.x < kChunks; ++k) {
         const int i = threadIdx.x * line.chunk + k;
         int L;
         if (i < a.n) mine += tiles_of(c, a, i, L);
@@ -192,22 +204,23 @@ __device__ int64_t build_line(const Kv4 &c, const Kv4Attn &a, Line &line, int64_
     if (lane == 31) sums[warp] = y;
     __syncthreads();
     for (int w = 0; w < warp; ++w) y += sums[w];
-    shared[threadIdx.x + 1] = y;
+    if (threadIdx.x < kChunks) shared[threadIdx.x + 1] = y;
     if (threadIdx.x == 0) shared[0] = 0;
     __syncthreads();
-    return shared[kMaxChunks];
+    return shared[kChunks];
 }
 
 // One tile of the line.
 struct Tile {
-    int uid, page, block;  // page -1: nothing to read
-    int edge;              // 1: first tile of its unit, 2: last
+    int64_t src;     // page * Hkv + head; -1: nothing to read
+    int uid, block;
+    int edge;        // 1: first tile of its unit, 2: last
 };
 template <int R>
 __device__ Tile locate(const Kv4 &c, const Kv4Attn &a, const Plan &p, const Line &line,
                        int64_t x) {
-    const int64_t y = x / p.units;
-    int lo = 0, hi = kMaxChunks;  // prefix[lo] <= y < prefix[hi]
+    const int64_t y = x < 0x7fffffff ? (uint32_t)x / (uint32_t)p.units : x / p.units;
+    int lo = 0, hi = kChunks;  // prefix[lo] <= y < prefix[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (line.prefix[mid] <= y) lo = mid;
@@ -217,11 +230,12 @@ __device__ Tile locate(const Kv4 &c, const Kv4Attn &a, const Plan &p, const Line
     int i = lo * line.chunk, L, T;
     while (base + (T = tiles_of(c, a, i, L)) <= y) base += T, ++i;
     const int64_t rem = x - base * p.units;
-    const int u = (int)(rem / T), t = (int)(rem - (int64_t)u * T);
+    const int u = (int)(rem < 0x7fffffff ? (uint32_t)rem / (uint32_t)T : rem / T);
+    const int t = (int)(rem - (int64_t)u * T);
     Tile tile;
     tile.uid = i * p.units + u;
     tile.edge = (t == 0 ? 1 : 0) | (t == T - 1 ? 2 : 0);
-    tile.page = -1;
+    tile.src = -1;
     const Unit un = unit_of<R>(c, a, p, tile.uid);
     const int blocks = (L + kBlock - 1) / kBlock;
     tile.block = t;
@@ -245,36 +259,127 @@ __device__ Tile locate(const Kv4 &c, const Kv4Attn &a, const Plan &p, const Line
     const int slot = kv4_slot(c, a.seqs, i);
     const int page = __ldg(c.table + (int64_t)slot * c.max_pages + tile.block);
     if (page < 0 || page >= c.n_pages) kv4_flag(a.status, SPARSTAR_STATUS_BAD_INDEX);
-    else tile.page = page;
+    else tile.src = (int64_t)page * c.Hkv + un.kh;
     return tile;
 }
 
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(kThreads, 1) few_kernel(Kv4 c, Kv4Attn a, Plan p) {
+// Running join of partial results: maximum, sum, four channels.
+struct Part4 {
+    float top = -INFINITY, sum = 0.0f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ void scale(float t) {  // to the maximum t >= top
+        const float f = top > -INFINITY ? ex2(top - t) : 0.0f;
+        top = t;
+        sum *= f;
+        acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+    }
+    __device__ void add(float m, float l, const float4 &x) {  // m <= top
+        const float f = m > -INFINITY ? ex2(m - top) : 0.0f;
+        sum = fmaf(f, l, sum);
+        acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+    }
+    // Ends the join: the result, or 0 where no token was seen.
+    template <typename T>
+    __device__ void write(T *out, float *lse) const {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        store(out, acc.x * inv), store(out + 1, acc.y * inv);
+        store(out + 2, acc.z * inv), store(out + 3, acc.w * inv);
+        if (lse) *lse = (top + log2f(sum)) * 0.6931471805599453f;
+    }
+};
+
+// The result of a unit whose partial results are the records of CTAs from ..
+// to, joined in that order whichever CTA runs this.  A thread has four
+// channels of a row; spare threads take the records in pieces.  Eight records
+// a step: their loads overlap.
+template <typename T, int D, int R, int kThreads>
+__device__ void join(const Plan &p, int from, int to, const Unit &u, const Kv4Attn &a,
+                     float *shared) {
+    constexpr int kRecord = R * (D + 2), kVecs = R * D / 4;
+    constexpr int kSplit = kThreads > kVecs ? kThreads / kVecs : 1;
+    const int n = to - from + 1;
+    const float *first = p.joins + ((int64_t)2 * from + 1) * kRecord;
+    const float *later = p.joins + (int64_t)2 * from * kRecord;  // + 2 kRecord a CTA
+    auto *piece = reinterpret_cast<Part4 *>(shared);             // [kSplit][kVecs]
+    for (int v = threadIdx.x; v < kVecs * kSplit; v += kThreads) {
+        const int vec = v % kVecs, row = vec / (D / 4), s = v / kVecs;
+        Part4 part;
+        const int k1 = n * (s + 1) / kSplit;
+        for (int k0 = n * s / kSplit; k0 < k1; k0 += 8) {
+            float m[8], l[8], top = part.top;
+            float4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                m[k] = -INFINITY, l[k] = 0.0f, x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + k >= k1) continue;
+                const float *rec = k0 + k ? later + (int64_t)(k0 + k) * 2 * kRecord : first;
+                m[k] = __ldcg(rec + R * D + row);
+                l[k] = __ldcg(rec + R * D + R + row);
+                x[k] = __ldcg(reinterpret_cast<const float4 *>(rec) + vec);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, m[k]);
+            part.scale(top);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) part.add(m[k], l[k], x[k]);
+        }
+        piece[v] = part;
+    }
+    __syncthreads();
+    for (int v = threadIdx.x; v < kVecs; v += kThreads) {
+        const int row = v / (D / 4), d = v % (D / 4) * 4;
+        if (row >= u.rows) continue;
+        Part4 part = piece[v];
+#pragma unroll
+        for (int s = 1; s < kSplit; ++s) {
+            const Part4 &o = piece[s * kVecs + v];
+            part.scale(fmaxf(part.top, o.top));
+            part.add(o.top, o.sum, o.acc);
+        }
+        part.write(static_cast<T *>(a.out) + (u.row + row) * D + d,
+                   d == 0 && a.lse ? a.lse + u.row + row : nullptr);
+    }
+}
+
+template <int D, int NT, bool F32, int kPair>
+__global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4Attn a, Plan p) {
     constexpr int R = 8 * NT;
+    constexpr int kThreads = 32 * kParts * kPair;
     constexpr int kTerms = F32 ? 3 : 1;
     constexpr int kHalf = kv4_half_bytes(D);
     constexpr int kCodes = kv4_code_bytes(D);
-    constexpr int kStages = D == 128 ? 3 : 6;  // half pages a warp keeps in flight
+    constexpr int kStages = D == 128 ? 3 : 6;  // half pages a part keeps in flight
     constexpr int KS = D / 16;                 // k steps of S^T, channel tiles of O^T
     constexpr int kRow = D + 4;                // joined rows: conflict-free stores
     using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t bars[kWarps][kStages];
-    __shared__ int64_t prefix[kMaxChunks + 1], sums[kWarps];
-    __shared__ int32_t last_uid[kWarps], last_edge[kWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ uint64_t full[kParts][kStages], empty[kParts][kStages];
+    __shared__ uint64_t given[kParts], taken[kParts];  // the pair's exchange
+    __shared__ int64_t prefix[kChunks + 1], sums[kParts * kPair];
+    // Partial results of the parts, in the order of the line: the end of a
+    // unit inside part k (2 k), what the part's end leaves (2 k + 1).
+    __shared__ int32_t entry[2 * kParts], edges[2 * kParts];
+    __shared__ int32_t cross[2], span[2][2], n_cross;
+    const int part = (threadIdx.x >> 5) / kPair, member = (threadIdx.x >> 5) % kPair;
+    const int lane = threadIdx.x & 31;
     const int r = lane >> 2, j = lane & 3;
-    // The joining kernel may start its launch; it waits for this one's end.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (lane == 0) {
-        for (int s = 0; s < kStages; ++s)
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&bars[warp][s]))
-                         : "memory");
+    const bool leads = member == 0;
+    if (lane == 0 && leads) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[part][s], 1);
+            mbar_init(&empty[part][s], kPair);
+        }
+        mbar_init(&given[part], 1);
+        mbar_init(&taken[part], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     Line line;
     const int64_t total = build_line(c, a, line, prefix, sums) * p.units;
+    // Tiles a CTA; CTA k has the tiles from k * share.
+    const int64_t share = total < 0x7fffffff - kCtas
+                              ? ((uint32_t)total + kCtas - 1) / kCtas
+                              : (total + kCtas - 1) / kCtas;
     // Sequences without tiles have no unit on the line.
     for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
         int L;
@@ -287,22 +392,22 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(Kv4 c, Kv4Attn a, Plan
         if (a.lse)
             for (int64_t k = threadIdx.x; k < rows; k += kThreads) a.lse[i * rows + k] = -INFINITY;
     }
-    // This warp's part [x, x1) of the line.
-    const int64_t c0 = total * blockIdx.x / kCtas, c1 = total * (blockIdx.x + 1) / kCtas;
-    // The warps' parts: equal, the last ones shorter or empty, so that parts
-    // with tiles are neighbours.
-    const int64_t part = (c1 - c0 + kWarps - 1) / kWarps;
-    int64_t x = min(c0 + part * warp, c1);
-    const int64_t x1 = min(x + part, c1);
-    const int slot_id = blockIdx.x * kWarps + warp;
-    const uint32_t ring = smem_u32(smem) + warp * kStages * kHalf;
-    const uint8_t *ring_ptr = smem + warp * kStages * kHalf;
+    // This part, [x, x1): an equal piece of the CTA's, the last ones shorter or
+    // empty.
+    const int64_t c0 = min(share * blockIdx.x, total), c1 = min(c0 + share, total);
+    const int64_t piece = ((uint32_t)(c1 - c0) + kParts - 1) / kParts;
+    int64_t x = min(c0 + piece * part, c1);
+    const int64_t x1 = min(x + piece, c1);
+    const int slot_id = blockIdx.x * kParts + part;
+    uint8_t *ring = smem + part * kStages * kHalf;
+    const uint32_t magic = kv4_magic();
+    const int tok0 = 32 * (r >> 1) + (r & 1);  // of row r, with 16 hp + 4 u, + 2 for r + 8
 
     // Tiles 32 at a time, one a lane; the next 32 are looked up ahead.
     Tile now, next;
     auto lookup = [&](int64_t at) {
         Tile t;
-        t.uid = t.page = -1;
+        t.src = t.uid = -1;
         t.block = t.edge = 0;
         if (at + lane < x1) t = locate<R>(c, a, p, line, at + lane);
         return t;
@@ -314,21 +419,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(Kv4 c, Kv4Attn a, Plan
     int64_t ix = x;       // next tile to copy
     int half_of = 0;      // its half: 0 keys, 1 values
     uint32_t issued = 0, used = 0;
+    bool ok = true;
     auto issue = [&]() {  // one half, if there is one in reach
         while (ix < x1 && ix < base + 64) {
             const int at = (int)(ix - base);
-            const int page = __shfl_sync(0xffffffffu, at < 32 ? now.page : next.page, at & 31);
-            if (page >= 0) {
-                const int uid = __shfl_sync(0xffffffffu, at < 32 ? now.uid : next.uid, at & 31);
-                if (lane == 0) {
-                    int rest = (uid % p.units) / p.row_tiles;
-                    const int kh = a.kv_cnt ? rest / p.nqb / p.heads : rest;
-                    const int s = issued % kStages;
-                    bulk_load(ring + s * kHalf,
-                              c.pages + ((int64_t)page * c.Hkv + kh) * (2 * kHalf) +
-                                  half_of * kHalf,
-                              kHalf, smem_u32(&bars[warp][s]));
-                }
+            const int64_t src =
+                __shfl_sync(0xffffffffu, at < 32 ? now.src : next.src, at & 31);
+            if (src >= 0) {
+                const int s = issued % kStages;
+                // Both warps of a pair have read what the stage held.
+                if (kPair > 1 && leads && issued >= kStages)
+                    ok = ok && wait_warp(&empty[part][s], (issued / kStages - 1) & 1u);
+                if (lane == 0 && leads && ok)
+                    bulk_load(smem_u32(ring + s * kHalf),
+                              c.pages + src * (2 * kHalf) + half_of * kHalf, kHalf,
+                              &full[part][s]);
                 ++issued;
                 if (half_of) ++ix;
                 half_of ^= 1;
@@ -338,6 +443,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(Kv4 c, Kv4Attn a, Plan
         }
     };
     for (int s = 0; s < kStages; ++s) issue();
+    auto release = [&]() {  // the oldest half is read; refill its stage
+        __syncwarp();
+        if (kPair > 1 && lane == 0) mbar_arrive(&empty[part][used % kStages]);
+        ++used;
+        issue();
+    };
 
     uint32_t q[kTerms][NT][KS][2];  // q^T: column r, channels of lane j
     float o[KS][NT][4];             // O^T: channels 16 k + r, + 8; rows 2 j, 2 j + 1
@@ -346,13 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(Kv4 c, Kv4Attn a, Plan
     int seen_min = 0;
     int uid = -1, started = 0;      // unit at work; it began with its first tile
     Unit un{};
-    bool ok = true;
-    if (lane == 0) {
-        p.head[slot_id] = p.head[kSlots + slot_id] = -1;
-        p.head[2 * kSlots + slot_id] = 0;
-        last_uid[warp] = -1;
-        last_edge[warp] = 0;
-    }
+    uint32_t joined = 0;            // exchanges of the pair
+    if (lane == 0 && leads) entry[2 * part] = entry[2 * part + 1] = -1;
 
     // Sums over the lanes that share rows.
     auto reduce_l = [&]() {
@@ -374,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(Kv4 c, Kv4Attn a, Plan
         }
         const int at = (int)(x - base);
         const int t_uid = __shfl_sync(0xffffffffu, now.uid, at);
-        const int t_page = __shfl_sync(0xffffffffu, now.page, at);
+        const bool t_has = __shfl_sync(0xffffffffu, (int)(now.src >= 0), at) != 0;
         const int t_block = __shfl_sync(0xffffffffu, now.block, at);
         const int t_edge = __shfl_sync(0xffffffffu, now.edge, at);
         if (t_uid != uid) {  // a unit begins (the one before it has been stored)
@@ -423,187 +529,264 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(Kv4 c, Kv4Attn a, Plan
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[k][nt][e] = 0.0f;
         }
-        if (t_page >= 0) {
+        if (t_has) {
             while (issued < used + 2 && issued - used < kStages) issue();
-            // ---------------------------------------------- S^T = K q^T
-            int st = used % kStages;
-            ok = wait_warp(smem_u32(&bars[warp][st]), (used / kStages) & 1u);
+            const int sk = used % kStages, sv = (used + 1) % kStages;
+            const uint32_t pv = ((used + 1) / kStages) & 1u;
+            const uint8_t *kp = ring + sk * kHalf, *vp = ring + sv * kHalf;
+            ok = ok && wait_warp(&full[part][sk], (used / kStages) & 1u);
             if (!ok) break;
-            const uint8_t *kp = ring_ptr + st * kHalf;
-            float s[8][NT][4];
+            // Half a page (64 tokens) at a time, each warp of a pair one; the
+            // loop is kept, as the whole page's code would not fit the
+            // instruction cache.
+#pragma unroll 1
+            for (int hp = kPair > 1 ? member : 0; hp < (kPair > 1 ? member + 1 : 2); ++hp) {
+                float s[4][NT][4];
+                // ------------------------------------------ S^T = K q^T
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.0f;
-                uint32_t w[2][D / 32], sc[2], mi[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int tok = 32 * (r >> 1) + 4 * u + (r & 1) + 2 * e;
-                    if constexpr (D == 128) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(kp + tok * 64 + j * 16);
-                        w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
-                        sc[e] = kv4_scale_pair(kp[kCodes + tok * 4 + j] * 0x10001u);
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(kp + tok * 32 + j * 8);
-                        w[e][0] = v.x, w[e][1] = v.y;
-                        sc[e] = kv4_scale_pair(kp[kCodes + tok * 2 + (j >> 1)] * 0x10001u);
-                    }
-                    mi[e] = kv4_minus136(sc[e]);
-                }
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t f[4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        f[e] = kv4_dequant(kv4_pair128(w[e][k / 2], 2 * (k % 2)), sc[e], mi[e]);
-                        f[2 + e] =
-                            kv4_dequant(kv4_pair128(w[e][k / 2], 2 * (k % 2) + 1), sc[e], mi[e]);
-                    }
-#pragma unroll
-                    for (int t = kTerms - 1; t >= 0; --t)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma(s[u][nt], f, q[t][nt][k][0], q[t][nt][k][1]);
-                }
-            }
-            __syncwarp();  // the keys' half is read: refill it
-            ++used;
-            issue();
-            // ------------------------------------------------- softmax
-            if ((t_block + 1) * kBlock > seen_min) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
+                for (int u = 0; u < 4; ++u) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int tok = t_block * kBlock + 32 * (r >> 1) + 4 * u + (r & 1) +
-                                            2 * (e >> 1);
-                            if (tok >= seen[nt][e & 1]) s[u][nt][e] = -INFINITY;
-                        }
-            }
-            uint32_t pw[kTerms][8][NT][2];  // P^T, tokens of the quad's lane j
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float neg[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
-#pragma unroll
-                    for (int u = 1; u < 8; ++u)
-                        mx = fmaxf(mx, fmaxf(s[u][nt][e], s[u][nt][e + 2]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float top = fmaxf(m[nt][e], mx * p.sc);
-                    const float f = top > m[nt][e] ? ex2(m[nt][e] - top) : 1.0f;
-                    m[nt][e] = top;
-                    l[nt][e] *= f;
-                    if (__any_sync(0xffffffffu, f != 1.0f)) {
-#pragma unroll
-                        for (int k = 0; k < KS; ++k) {
-                            o[k][nt][e] *= f;
-                            o[k][nt][e + 2] *= f;
-                        }
-                    }
-                    // While every token was masked, every weight is 0.
-                    neg[e] = top > -INFINITY ? -top : 0.0f;
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[u][nt][e] = ex2(fmaf(s[u][nt][e], p.sc, neg[e & 1]));
-                        l[nt][e & 1] += s[u][nt][e];
-                    }
-#pragma unroll
-                    for (int t = 0; t < kTerms; ++t)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            pw[t][u][nt][e] = transpose8x8(
-                                t + 1 < kTerms ? split(s[u][nt][2 * e], s[u][nt][2 * e + 1])
-                                               : pack(s[u][nt][2 * e], s[u][nt][2 * e + 1]));
-                }
-            }
-            // --------------------------------------------- O^T += V^T P^T
-            st = used % kStages;
-            ok = wait_warp(smem_u32(&bars[warp][st]), (used / kStages) & 1u);
-            if (!ok) break;
-            const uint8_t *vp = ring_ptr + st * kHalf;
-#pragma unroll
-            for (int g = 0; g < D / kGroup; ++g) {
-                uint32_t sc[16], mi[16];  // of token pairs 32 j + 2 i
-                {
-                    const uint4 *sp = reinterpret_cast<const uint4 *>(vp + kCodes + g * kBlock +
-                                                                      32 * j);
-                    const uint4 v0 = sp[0], v1 = sp[1];
-                    const uint32_t b[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        sc[i] = kv4_scale_pair(
-                            __byte_perm(b[i / 2], 0, (i & 1) ? 0x4342 : 0x4140));
-                        mi[i] = kv4_minus136(sc[i]);
-                    }
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int k = 2 * g + half;
-                    uint32_t w[2][4];
+                        for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.0f;
+                    uint32_t w[2][D / 32], sc[2], mi[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            vp + (16 * k + r + 8 * e) * 64 + j * 16);
-                        w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
+                        const int tok = tok0 + 16 * hp + 4 * u + 2 * e;
+                        if constexpr (D == 128) {
+                            const uint4 v =
+                                *reinterpret_cast<const uint4 *>(kp + tok * 64 + j * 16);
+                            w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
+                            sc[e] = kv4_scale_pair(kp[kCodes + tok * 4 + j] * 0x10001u);
+                        } else {
+                            const uint2 v =
+                                *reinterpret_cast<const uint2 *>(kp + tok * 32 + j * 8);
+                            w[e][0] = v.x, w[e][1] = v.y;
+                            sc[e] = kv4_scale_pair(kp[kCodes + tok * 2 + (j >> 1)] * 0x10001u);
+                        }
+                        mi[e] = kv4_minus136(sc[e]);
                     }
-                    // fp32: the page's sum apart, joined by rounded additions
-                    // (the tensor core's own additions truncate).
-                    float part[NT][4];
-                    if constexpr (F32) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) part[nt][e] = 0.0f;
-                    }
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
+                    for (int k = 0; k < KS; ++k) {
                         uint32_t f[4];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            f[e] = kv4_dequant(kv4_pair128(w[e][u / 2], 2 * (u % 2)), sc[2 * u],
-                                               mi[2 * u]);
-                            f[2 + e] = kv4_dequant(kv4_pair128(w[e][u / 2], 2 * (u % 2) + 1),
-                                                   sc[2 * u + 1], mi[2 * u + 1]);
-                        }
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                f[2 * h + e] = kv4_dequant(
+                                    kv4_pair128(w[e][k / 2], 2 * (k % 2) + h, magic), sc[e],
+                                    mi[e]);
 #pragma unroll
                         for (int t = kTerms - 1; t >= 0; --t)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                if constexpr (F32)
-                                    mma(part[nt], f, pw[t][u][nt][0], pw[t][u][nt][1]);
-                                else
-                                    mma(o[k][nt], f, pw[t][u][nt][0], pw[t][u][nt][1]);
-                            }
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma(s[u][nt], f, q[t][nt][k][0], q[t][nt][k][1]);
                     }
-                    if constexpr (F32) {
+                }
+                if (kPair > 1 || hp == 1) release();  // the keys
+                // --------------------------------------------- softmax
+                if ((t_block + 1) * kBlock > seen_min) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[k][nt][e] += part[nt][e];
+                            for (int e = 0; e < 4; ++e) {
+                                const int tok = t_block * kBlock + tok0 + 16 * hp + 4 * u +
+                                                2 * (e >> 1);
+                                if (tok >= seen[nt][e & 1]) s[u][nt][e] = -INFINITY;
+                            }
+                }
+                uint32_t pw[kTerms][4][NT][2];  // P^T, tokens of the quad's lane j
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float neg[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
+#pragma unroll
+                        for (int u = 1; u < 4; ++u)
+                            mx = fmaxf(mx, fmaxf(s[u][nt][e], s[u][nt][e + 2]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float top = fmaxf(m[nt][e], mx * p.sc);
+                        if (__any_sync(0xffffffffu, top > m[nt][e])) {
+                            const float f = top > m[nt][e] ? ex2(m[nt][e] - top) : 1.0f;
+                            m[nt][e] = top;
+                            l[nt][e] *= f;
+#pragma unroll
+                            for (int k = 0; k < KS; ++k) {
+                                o[k][nt][e] *= f;
+                                o[k][nt][e + 2] *= f;
+                            }
+                        }
+                        // While every token was masked, every weight is 0.
+                        neg[e] = top > -INFINITY ? -top : 0.0f;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s[u][nt][e] = ex2(fmaf(s[u][nt][e], p.sc, neg[e & 1]));
+                            l[nt][e & 1] += s[u][nt][e];
+                        }
+#pragma unroll
+                        for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                pw[t][u][nt][e] = transpose8x8(
+                                    t + 1 < kTerms
+                                        ? split(s[u][nt][2 * e], s[u][nt][2 * e + 1])
+                                        : pack(s[u][nt][2 * e], s[u][nt][2 * e + 1]));
+                    }
+                }
+                // ------------------------------------- O^T += V^T P^T
+                if (kPair > 1 || hp == 0) {
+                    ok = ok && wait_warp(&full[part][sv], pv);
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int g = 0; g < D / kGroup; ++g) {
+                    uint32_t sc[8], mi[8];  // of token pairs 32 j + 16 hp + 2 i
+                    {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            vp + kCodes + g * kBlock + 32 * j + 16 * hp);
+                        const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            sc[i] = kv4_scale_pair(
+                                __byte_perm(b[i / 2], 0, (i & 1) ? 0x4342 : 0x4140));
+                            mi[i] = kv4_minus136(sc[i]);
+                        }
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int k = 2 * g + half;
+                        uint32_t w[2][2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(
+                                vp + (16 * k + r + 8 * e) * 64 + j * 16 + 8 * hp);
+                            w[e][0] = v.x, w[e][1] = v.y;
+                        }
+                        // fp32: the sum of 64 tokens apart, joined by rounded
+                        // additions (the tensor core's own ones truncate).
+                        float part[NT][4];
+                        if constexpr (F32) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) part[nt][e] = 0.0f;
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t f[4];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    f[2 * h + e] = kv4_dequant(
+                                        kv4_pair128(w[e][u / 2], 2 * (u % 2) + h, magic),
+                                        sc[2 * u + h], mi[2 * u + h]);
+#pragma unroll
+                            for (int t = kTerms - 1; t >= 0; --t)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    if constexpr (F32)
+                                        mma(part[nt], f, pw[t][u][nt][0], pw[t][u][nt][1]);
+                                    else
+                                        mma(o[k][nt], f, pw[t][u][nt][0], pw[t][u][nt][1]);
+                                }
+                        }
+                        if constexpr (F32) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[k][nt][e] += part[nt][e];
+                        }
                     }
                 }
             }
-            __syncwarp();
-            ++used;
-            issue();
+            if (!ok) break;
+            release();  // the values
         }
         ++x;
         const bool ends = (t_edge & 2) != 0;
         if (x < x1 && !ends) continue;
-        // The unit ends here, or this warp's part does.
+        // The unit ends here, or the part does.
         reduce_l();
-        if (ends && started) {  // whole: straight to the output
+        if (x == x1) {  // what the part's end leaves stays in registers
+            if (lane == 0 && leads) {
+                entry[2 * part + 1] = uid;
+                edges[2 * part + 1] = started | (t_edge & 2);
+            }
+            break;
+        }
+        if constexpr (kPair > 1) {
+            // The pair's results join in the leading warp, a quarter of the
+            // accumulator at a time.
+            float4 *box = reinterpret_cast<float4 *>(smem + kParts * kStages * kHalf) +
+                          part * (KS / 4 + 1) * NT * 32 + lane;
+            float fa[NT][2], fb[NT][2];
+#pragma unroll
+            for (int qt = 0; qt < 4 && ok; ++qt) {
+                if (!leads) {
+                    if (joined) ok = wait_warp(&taken[part], (joined - 1) & 1u);
+                    if (!ok) break;
+                    if (qt == 0) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            box[(KS / 4 * NT + nt) * 32] =
+                                make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < KS / 4; ++k)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float(&v)[4] = o[qt * KS / 4 + k][nt];
+                            box[(k * NT + nt) * 32] = make_float4(v[0], v[1], v[2], v[3]);
+                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&given[part]);
+                } else {
+                    ok = wait_warp(&given[part], joined & 1u);
+                    if (!ok) break;
+                    if (qt == 0) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float4 b = box[(KS / 4 * NT + nt) * 32];
+                            const float mb[2] = {b.x, b.y}, lb[2] = {b.z, b.w};
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float top = fmaxf(m[nt][e], mb[e]);
+                                fa[nt][e] = m[nt][e] > -INFINITY ? ex2(m[nt][e] - top) : 0.0f;
+                                fb[nt][e] = mb[e] > -INFINITY ? ex2(mb[e] - top) : 0.0f;
+                                l[nt][e] = l[nt][e] * fa[nt][e] + lb[e] * fb[nt][e];
+                                m[nt][e] = top;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < KS / 4; ++k)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float(&v)[4] = o[qt * KS / 4 + k][nt];
+                            const float4 b = box[(k * NT + nt) * 32];
+                            v[0] = v[0] * fa[nt][0] + b.x * fb[nt][0];
+                            v[1] = v[1] * fa[nt][1] + b.y * fb[nt][1];
+                            v[2] = v[2] * fa[nt][0] + b.z * fb[nt][0];
+                            v[3] = v[3] * fa[nt][1] + b.w * fb[nt][1];
+                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&taken[part]);
+                }
+                ++joined;
+            }
+            if (!ok) break;
+        }
+        if (!leads) {
+        } else if (started) {  // whole: straight to the output
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -621,8 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(Kv4 c, Kv4Attn a, Plan
                         a.lse[un.row + row] =
                             (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
                 }
-        } else if (x < x1) {  // the end of a unit that began before this part
-            float *rec = p.records + ((int64_t)slot_id * 2 + 1) * R * (D + 2);
+        } else {  // the end of a unit that began before this part
+            float *rec = p.ends + (int64_t)slot_id * R * (D + 2);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -638,155 +821,142 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(Kv4 c, Kv4Attn a, Plan
                         rec[R * D + R + row] = l[nt][e];
                     }
                 }
-            if (lane == 0) p.head[kSlots + slot_id] = uid;
-        } else if (lane == 0) {
-            last_uid[warp] = uid;
-            last_edge[warp] = started | (ends ? 2 : 0);
+            if (lane == 0) {
+                entry[2 * part] = uid;
+                edges[2 * part] = 2;
+            }
         }
-        if (ends) uid = -1;
+        uid = -1;
     }
     // Copies in flight land before anything else uses the ring.
     while (used < issued) {
-        if (!wait_warp(smem_u32(&bars[warp][used % kStages]), (used / kStages) & 1u)) ok = false;
+        if (!wait_warp(&full[part][used % kStages], (used / kStages) & 1u)) ok = false;
         ++used;
     }
     if (!ok && lane == 0) kv4_flag(a.status, SPARSTAR_STATUS_TIMEOUT);
 
-    // ---------------------- partial results at the parts' ends, CTA by CTA
+    // ------------------------------ the parts' partial results, unit by unit
     __syncthreads();
-    float *so = reinterpret_cast<float *>(smem);       // [kWarps][R][kRow]
-    float *sm = so + kWarps * R * kRow, *sl = sm + kWarps * R;
-    if (last_uid[warp] >= 0) {
+    constexpr int kRecord = R * (D + 2);
+    constexpr int kWarps = kParts * kPair, kHeld = kWarps + kParts;
+    // What each warp's registers hold, then the ends inside parts: [kHeld].
+    float *so = reinterpret_cast<float *>(smem);  // [kHeld][R][kRow]
+    float *sm = so + kHeld * R * kRow, *sl = sm + kHeld * R;
+    if (entry[2 * part + 1] >= 0) {
+        const int w = part * kPair + member;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = nt * 8 + 2 * j + e;
-                float *dst = so + (warp * R + row) * kRow + r;
+                float *dst = so + (w * R + row) * kRow + r;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     dst[16 * k] = o[k][nt][e];
                     dst[16 * k + 8] = o[k][nt][e + 2];
                 }
                 if (r == 0) {
-                    sm[warp * R + row] = m[nt][e];
-                    sl[warp * R + row] = l[nt][e];
+                    sm[w * R + row] = m[nt][e];
+                    sl[w * R + row] = l[nt][e];
                 }
             }
     }
+    if (leads && entry[2 * part] >= 0) {
+        const float *rec = p.ends + (int64_t)slot_id * kRecord;
+        const int w = kWarps + part;
+        for (int v = lane; v < R * D / 4; v += 32)
+            *reinterpret_cast<float4 *>(so + (w * R + v / (D / 4)) * kRow + v % (D / 4) * 4) =
+                *reinterpret_cast<const float4 *>(rec + 4 * v);
+        if (lane < R) {
+            sm[w * R + lane] = rec[R * D + lane];
+            sl[w * R + lane] = rec[R * D + R + lane];
+        }
+    }
+    if (threadIdx.x == 0) n_cross = 0;
     __syncthreads();
-    for (int w0 = 0; w0 < kWarps;) {
-        const int id = last_uid[w0];
-        int w1 = w0 + 1;
-        while (w1 < kWarps && id >= 0 && last_uid[w1] == id) ++w1;
-        if (id >= 0) {
-            const bool begins = (last_edge[w0] & 1) != 0;
-            const bool whole = begins && (last_edge[w1 - 1] & 2);
-            const Unit g = unit_of<R>(c, a, p, id);
-            float *rec = p.records + (int64_t)(blockIdx.x * kWarps + w0) * 2 * R * (D + 2);
-            for (int it = threadIdx.x; it < R * D; it += kThreads) {
-                const int row = it / D, d = it % D;
-                float top = -INFINITY, sum = 0.0f, acc = 0.0f;
-                for (int w = w0; w < w1; ++w) top = fmaxf(top, sm[w * R + row]);
-                for (int w = w0; w < w1; ++w) {
-                    const float mw = sm[w * R + row];
-                    const float f = mw > -INFINITY ? ex2(mw - top) : mw == mw ? 0.0f : mw;
-                    sum = fmaf(f, sl[w * R + row], sum);
-                    acc = fmaf(f, so[(w * R + row) * kRow + d], acc);
+    for (int e0 = 0; e0 < 2 * kParts;) {
+        const int id = entry[e0];
+        if (id < 0) {
+            ++e0;
+            continue;
+        }
+        int e1 = e0 + 1, last = e0;  // entries e0 .. last are this unit's, or empty
+        uint32_t mine = 1u << e0;
+        for (; e1 < 2 * kParts && (entry[e1] == id || entry[e1] < 0); ++e1)
+            if (entry[e1] == id) last = e1, mine |= 1u << e1;
+        const bool begins = (edges[e0] & 1) != 0, whole = begins && (edges[last] & 2);
+        const Unit g = unit_of<R>(c, a, p, id);
+        float *rec = p.joins + (int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * kRecord;
+        for (int v = threadIdx.x; v < R * D / 4; v += kThreads) {
+            const int row = v / (D / 4), d = v % (D / 4) * 4;
+            Part4 sum;
+            float top = -INFINITY;
+            auto each = [&](auto f) {
+                for (uint32_t left = mine; left; left &= left - 1) {
+                    const int en = __ffs(left) - 1;
+                    if (en & 1) {
+#pragma unroll
+                        for (int w = 0; w < kPair; ++w) f((en >> 1) * kPair + w);
+                    } else {
+                        f(kWarps + (en >> 1));
+                    }
                 }
-                if (!whole) {
-                    rec[row * D + d] = acc;
-                    if (d == 0) rec[R * D + row] = top, rec[R * D + R + row] = sum;
-                } else if (row < g.rows) {
-                    store(static_cast<T *>(a.out) + (g.row + row) * D + d,
-                          sum == 0.0f ? 0.0f : acc / sum);
-                    if (d == 0 && a.lse)
-                        a.lse[g.row + row] = (top + log2f(sum)) * 0.6931471805599453f;
-                }
-            }
-            if (!whole && threadIdx.x == 0) {
-                for (int w = w0; w < w1; ++w) {
-                    p.head[blockIdx.x * kWarps + w] = id;
-                    p.head[2 * kSlots + blockIdx.x * kWarps + w] =
-                        (last_edge[w] & 2) | (w == w0 && begins ? 1 : 0);
-                }
+            };
+            each([&](int w) { top = fmaxf(top, sm[w * R + row]); });
+            sum.top = top;
+            each([&](int w) {
+                sum.add(sm[w * R + row], sl[w * R + row],
+                        *reinterpret_cast<const float4 *>(so + (w * R + row) * kRow + d));
+            });
+            if (!whole) {
+                *reinterpret_cast<float4 *>(rec + 4 * v) = sum.acc;
+                if (d == 0) rec[R * D + row] = sum.top, rec[R * D + R + row] = sum.sum;
+            } else if (row < g.rows) {
+                sum.write(static_cast<T *>(a.out) + (g.row + row) * D + d,
+                          d == 0 && a.lse ? a.lse + g.row + row : nullptr);
             }
         }
-        w0 = w1;
+        if (!whole && threadIdx.x == 0) cross[n_cross++] = id;
+        e0 = last + 1;
+    }
+    // ---------------- units of several CTAs: the last one to arrive joins them
+    __syncthreads();
+    if (threadIdx.x < n_cross) {
+        const int id = cross[threadIdx.x], i = id / p.units;
+        int64_t first = line.prefix[i / line.chunk];
+        int L;
+        for (int s = i / line.chunk * line.chunk; s < i; ++s) first += tiles_of(c, a, s, L);
+        const int tiles = tiles_of(c, a, i, L);
+        first = first * p.units + (int64_t)(id - i * p.units) * tiles;
+        const int from = (int)(first / share), to = (int)((first + tiles - 1) / share);
+        __threadfence();
+        const bool last = atomicAdd(p.arrived + from, 1u) == (uint32_t)(to - from);
+        if (last) p.arrived[from] = 0;
+        __threadfence();
+        span[threadIdx.x][0] = last ? from : -1;
+        span[threadIdx.x][1] = to;
+    }
+    __syncthreads();
+    for (int k = 0; k < n_cross; ++k) {
+        if (span[k][0] < 0) continue;
+        join<T, D, R, kThreads>(p, span[k][0], span[k][1], unit_of<R>(c, a, p, cross[k]), a,
+                                reinterpret_cast<float *>(smem));
+        __syncthreads();
     }
 }
 
-// Joins the partial results of the units that no CTA finished: block b takes
-// the one that begins in warp part b, if there is one; a warp a row.
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(256 * NT) join_kernel(Kv4 c, Kv4Attn a, Plan p) {
-    constexpr int R = 8 * NT, V = D / 32;
-    using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.x;
-    if (!(p.head[2 * kSlots + b] & 1)) return;
-    const int id = p.head[b];
-    const Unit u = unit_of<R>(c, a, p, id);
-    const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // Records: this one, the first of every later CTA that has the unit, and
-    // the end of the unit inside a part.
-    float top = -INFINITY, sum = 0.0f, acc[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    auto add = [&](const float *rec) {
-        const float mw = rec[R * D + row], lw = rec[R * D + R + row];
-        float x[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[v] = rec[row * D + 32 * v + lane];
-        const float t = fmaxf(top, mw);
-        const float f = top > -INFINITY ? ex2(top - t) : 0.0f;
-        const float g = mw > -INFINITY ? ex2(mw - t) : mw == mw ? 0.0f : mw;
-        top = t;
-        sum = fmaf(g, lw, sum * f);
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(g, x[v], acc[v] * f);
-    };
-    add(p.records + (int64_t)b * 2 * R * (D + 2));
-    int cta = b / kWarps;  // the latest CTA whose record is in
-    for (int s = b + 1; s < kSlots; ++s) {
-        if (p.head[s] == id) {
-            if (s / kWarps != cta) add(p.records + (int64_t)s * 2 * R * (D + 2));
-            cta = s / kWarps;
-            if (p.head[2 * kSlots + s] & 2) break;
-        } else if (p.head[kSlots + s] == id) {
-            add(p.records + ((int64_t)s * 2 + 1) * R * (D + 2));
-            break;
-        }  // else a part without tiles, between parts that have some
-    }
-    if (row >= u.rows) return;
-    T *dst = static_cast<T *>(a.out) + (u.row + row) * D + lane;
-#pragma unroll
-    for (int v = 0; v < V; ++v) store(dst + 32 * v, sum == 0.0f ? 0.0f : acc[v] / sum);
-    if (a.lse && lane == 0) a.lse[u.row + row] = (top + log2f(sum)) * 0.6931471805599453f;
-}
-
-template <int D, int NT, bool F32>
+template <int D, int NT, bool F32, int kPair>
 cudaError_t launch(const Kv4 &c, const Kv4Attn &a, const Plan &p, cudaStream_t stream) {
-    constexpr int kRing = kWarps * (D == 128 ? 3 : 6) * kv4_half_bytes(D);
-    constexpr int kJoin = kWarps * 8 * NT * (D + 4 + 2) * 4;
+    constexpr int kBox = kPair > 1 ? kParts * (D / 64 + 1) * NT * 32 * 16 : 0;
+    constexpr int kRing = kParts * (D == 128 ? 3 : 6) * kv4_half_bytes(D) + kBox;
+    constexpr int kJoin = kParts * (kPair + 1) * 8 * NT * (D + 4 + 2) * 4;
     constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
-    cudaError_t e = cudaFuncSetAttribute(few_kernel<D, NT, F32>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    const auto kernel = few_kernel<D, NT, F32, kPair>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
-    few_kernel<D, NT, F32><<<kCtas, kThreads, kBytes, stream>>>(c, a, p);
-    // The joining kernel is set up while this one runs (it waits for its end
-    // before it reads anything).
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kSlots);
-    cfg.blockDim = dim3(256 * NT);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, join_kernel<D, NT, F32>, c, a, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    kernel<<<kCtas, 32 * kParts * kPair, kBytes, stream>>>(c, a, p);
+    return cudaGetLastError();
 }
 
 int stripe_rows(int64_t Hq, int64_t Hkv, int64_t Lq, bool lists) {
@@ -796,7 +966,7 @@ int stripe_rows(int64_t Hq, int64_t Hkv, int64_t Lq, bool lists) {
 }  // namespace
 
 int64_t kv4_attn_few_work_bytes(int D) {
-    return 3 * kSlots * 4 + (int64_t)kSlots * 2 * 16 * (D + 2) * 4;
+    return kArrivedBytes + (int64_t)(2 * kCtas + kSlots) * 16 * (D + 2) * 4;
 }
 
 cudaError_t launch_kv4_attn_few(const Kv4 &c, const Kv4Attn &a, int dtype, cudaStream_t stream) {
@@ -815,15 +985,17 @@ cudaError_t launch_kv4_attn_few(const Kv4 &c, const Kv4Attn &a, int dtype, cudaS
     // every score below 2^-90.
     p.sc = fmaxf(fabsf(a.tau) * 1.4426950408889634f, 1e-37f);
     p.flip = a.tau < 0.0f ? 0x80008000u : 0u;
-    p.head = static_cast<int32_t *>(a.work);
-    p.records = reinterpret_cast<float *>(p.head + 3 * kSlots);
+    p.arrived = static_cast<uint32_t *>(a.work);
+    p.joins = static_cast<float *>(a.work) + kArrivedBytes / 4;
+    p.ends = p.joins + (int64_t)2 * kCtas * R * (c.D + 2);
     if (c.D == 128) {
-        if (f32) return launch<128, 1, true>(c, a, p, stream);
-        return R == 8 ? launch<128, 1, false>(c, a, p, stream)
-                      : launch<128, 2, false>(c, a, p, stream);
+        if (f32) return launch<128, 1, true, 1>(c, a, p, stream);
+        return R == 8 ? launch<128, 1, false, 2>(c, a, p, stream)
+                      : launch<128, 2, false, 1>(c, a, p, stream);
     }
-    if (f32) return launch<64, 1, true>(c, a, p, stream);
-    return R == 8 ? launch<64, 1, false>(c, a, p, stream) : launch<64, 2, false>(c, a, p, stream);
+    if (f32) return launch<64, 1, true, 1>(c, a, p, stream);
+    return R == 8 ? launch<64, 1, false, 2>(c, a, p, stream)
+                  : launch<64, 2, false, 1>(c, a, p, stream);
 }
 
 }  // namespace sparstar

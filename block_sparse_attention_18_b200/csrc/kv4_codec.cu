@@ -204,7 +204,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, uint32_t w, uint32_t co
     const uint32_t s = kv4_scale_pair(code * 0x10001u), m = kv4_minus136(s);
     uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = kv4_dequant(kv4_pair128(w, i), s, m);
+    for (int i = 0; i < 4; ++i) o[i] = kv4_dequant(kv4_pair128(w, i, kMagic), s, m);
     *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 __device__ __forceinline__ void store8(float *p, uint32_t w, uint32_t code) {

@@ -22,6 +22,7 @@ STATUS_TIMEOUT = 0x2
 STATUS_NO_PAGES = 0x4
 STATUS_CLAMPED = 0x8
 STATUS_SHARED = 0x10
+KV4_WORK_ZEROS = 1024
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 
@@ -459,9 +460,25 @@ class Kv4Cache:
         self.pages, self.refs, self.table, self.lens, self.work = pages, refs, table, lens, work
         self.n_pages, self.n_seqs, self.max_pages = n_pages, n_seqs, table.shape[1]
         self.Hkv, self.D, self.device = pages.shape[1], D, pages.device
+        self.index = pages.get_device()
+        self._work_of = {}  # stream handle -> scratch of its attention calls
         self._struct = _Kv4Struct(pages.data_ptr(), refs.data_ptr(), table.data_ptr(),
                                   lens.data_ptr(), work.data_ptr(), n_pages, n_seqs,
                                   table.shape[1], pages.shape[1], D)
+
+    def _attn_work(self, need: int, stream: int):
+        """Scratch for attention calls on this stream, the current one."""
+        if torch.cuda.is_current_stream_capturing():
+            return self._new_work(need)
+        work = self._work_of.get(stream)
+        if work is None or work.numel() < need:
+            work = self._work_of[stream] = self._new_work(need)
+        return work
+
+    def _new_work(self, need: int):
+        work = torch.empty(need, dtype=torch.uint8, device=self.device)
+        work[:KV4_WORK_ZEROS].zero_()
+        return work
 
     @classmethod
     def empty(cls, n_pages: int, n_seqs: int, max_pages: int, Hkv: int, D: int, device="cuda"):
@@ -474,22 +491,22 @@ class Kv4Cache:
                    torch.zeros(n_seqs, **i32), D)
 
 
-def _kv4_ints(cache, t, name, n=None):
-    """A device list of int32 (or None): its pointer."""
+def _kv4_ints(cache, t, name, n):
+    """A device list of n int32 (or None): its pointer."""
     if t is None:
         return None
-    _dev(t, name, torch.int32)
-    if t.device != cache.device or t.dim() != 1 or (n is not None and t.numel() != n):
-        raise ValueError("%s must be int32 [%s] on %s" % (name, "n" if n is None else n,
-                                                          cache.device))
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n \
+            or t.get_device() != cache.index or not t.is_contiguous():
+        raise ValueError("%s must be contiguous int32 [%d] on %s" % (name, n, cache.device))
     return t.data_ptr()
 
 
 def _kv4_tensor(cache, t, name, dtype, shape):
-    _dev(t, name, dtype)
-    if t.device != cache.device or tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s on %s, got %s on %s"
-                         % (name, tuple(shape), cache.device, tuple(t.shape), t.device))
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != cache.index \
+            or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s %s on %s, got %s %s on %s"
+                         % (name, dtype, tuple(shape), cache.device, t.dtype, tuple(t.shape),
+                            t.device))
     return t.data_ptr()
 
 
@@ -498,23 +515,29 @@ def _kv4_status(cache, status):
 
 
 class _Kv4Call:
-    """The device of the cache and the stream of a call, as context."""
+    """Context of a call: the cache's device is the current one, and so is the
+    stream given; yields the stream's handle."""
+
+    __slots__ = ("device", "stream", "index")
 
     def __init__(self, cache, stream):
-        self.guard = None
-        if torch.cuda.current_device() != cache.device.index:
-            self.guard = torch.cuda.device(cache.device)
-        self.given = stream
+        self.index = cache.index
+        self.device = torch.cuda.device(cache.index) \
+            if torch._C._cuda_getDevice() != cache.index else None
+        self.stream = None if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        s = self.given if self.given is not None else torch.cuda.current_stream()
-        return s
+        if self.device is not None:
+            self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
         return False
 
 
@@ -523,8 +546,8 @@ def sparstar_kv4_resize(cache: Kv4Cache, new_lens, seqs=None, status=None, strea
     n = new_lens.numel()
     with _Kv4Call(cache, stream) as s:
         _check(lib.sparstar_kv4_resize(cache._struct, _kv4_ints(cache, seqs, "seqs", n),
-                                       _kv4_ints(cache, new_lens, "new_lens"), n,
-                                       _kv4_status(cache, status), s.cuda_stream),
+                                       _kv4_ints(cache, new_lens, "new_lens", n), n,
+                                       _kv4_status(cache, status), s),
                "sparstar_kv4_resize")
 
 
@@ -533,10 +556,10 @@ def sparstar_kv4_fork(cache: Kv4Cache, src, dst, lens=None, deep: bool = False, 
     """Empty sequences dst take the tokens of src: shared pages, or (deep) copies."""
     n = src.numel()
     with _Kv4Call(cache, stream) as s:
-        _check(lib.sparstar_kv4_fork(cache._struct, _kv4_ints(cache, src, "src"),
+        _check(lib.sparstar_kv4_fork(cache._struct, _kv4_ints(cache, src, "src", n),
                                      _kv4_ints(cache, dst, "dst", n),
                                      _kv4_ints(cache, lens, "lens", n), n, int(bool(deep)),
-                                     _kv4_status(cache, status), s.cuda_stream),
+                                     _kv4_status(cache, status), s),
                "sparstar_kv4_fork")
 
 
@@ -544,19 +567,11 @@ def sparstar_kv4_compact(cache: Kv4Cache, n_live=None, stream=None):
     """Moves the live pages to the lowest places; returns their number (device)."""
     with _Kv4Call(cache, stream) as s:
         if n_live is None:
-            n_live = _kv4_new(s, (1,), torch.int32, cache.device)
+            n_live = torch.empty(1, dtype=torch.int32, device=cache.device)
         _check(lib.sparstar_kv4_compact(cache._struct,
                                         _kv4_tensor(cache, n_live, "n_live", torch.int32, (1,)),
-                                        s.cuda_stream), "sparstar_kv4_compact")
+                                        s), "sparstar_kv4_compact")
     return n_live
-
-
-def _kv4_new(stream, shape, dtype, device):
-    """A tensor of the stream that the call runs on."""
-    if stream == torch.cuda.current_stream():
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def sparstar_kv4_write(cache: Kv4Cache, k, v, seqs=None, starts=None, counts=None, status=None,
@@ -567,13 +582,13 @@ def sparstar_kv4_write(cache: Kv4Cache, k, v, seqs=None, starts=None, counts=Non
     n, _, T, _ = k.shape
     shape = (n, cache.Hkv, T, cache.D)
     with _Kv4Call(cache, stream) as s:
-        _check(lib.sparstar_kv4_write(cache._struct, _kv4_tensor(cache, k, "k", None, shape),
+        _check(lib.sparstar_kv4_write(cache._struct, _kv4_tensor(cache, k, "k", k.dtype, shape),
                                       _kv4_tensor(cache, v, "v", k.dtype, shape),
                                       _DTYPE.get(k.dtype, -1), n, T,
                                       _kv4_ints(cache, seqs, "seqs", n),
                                       _kv4_ints(cache, starts, "starts", n),
                                       _kv4_ints(cache, counts, "counts", n),
-                                      _kv4_status(cache, status), s.cuda_stream),
+                                      _kv4_status(cache, status), s),
                "sparstar_kv4_write")
 
 
@@ -591,17 +606,15 @@ def sparstar_kv4_read(cache: Kv4Cache, T: int, n: int = None, dtype=torch.bfloat
         dtype = (k if k is not None else v).dtype
     with _Kv4Call(cache, stream) as s:
         if k is None and v is None:
-            k, v = (_kv4_new(s, shape, dtype, cache.device) for _ in range(2))
-            if counts is not None:
-                with torch.cuda.stream(s):
-                    k.zero_(), v.zero_()
+            new = torch.empty if counts is None else torch.zeros
+            k, v = (new(shape, dtype=dtype, device=cache.device) for _ in range(2))
         kp = None if k is None else _kv4_tensor(cache, k, "k", dtype, shape)
         vp = None if v is None else _kv4_tensor(cache, v, "v", dtype, shape)
         _check(lib.sparstar_kv4_read(cache._struct, kp, vp, _DTYPE.get(dtype, -1), n, T,
                                      _kv4_ints(cache, seqs, "seqs", n),
                                      _kv4_ints(cache, starts, "starts", n),
                                      _kv4_ints(cache, counts, "counts", n),
-                                     _kv4_status(cache, status), s.cuda_stream),
+                                     _kv4_status(cache, status), s),
                "sparstar_kv4_read")
     return k, v
 
@@ -615,7 +628,9 @@ def sparstar_kv4_attn(cache: Kv4Cache, q, seqs=None, tau: float = None, causal: 
                       kv_idx=None, kv_cnt=None, out=None, lse=None, want_lse: bool = True,
                       work=None, status=None, stream=None):
     """Attention of q [n, Hq, Lq, D] over the cached tokens of n sequences;
-    returns (out, lse).  ``work`` (uint8) is allocated when not given."""
+    returns (out, lse).  ``work`` (uint8, its first KV4_WORK_ZEROS bytes zero
+    before its first use): when not given, the cache keeps one a stream, and a
+    call that is captured into a graph gets one of its own."""
     if q.dim() != 4:
         raise ValueError("q must be [n, Hq, Lq, D]")
     n, Hq, Lq, D = q.shape
@@ -624,38 +639,39 @@ def sparstar_kv4_attn(cache: Kv4Cache, q, seqs=None, tau: float = None, causal: 
         raise ValueError("q has head dim %d, the cache %d" % (D, cache.D))
     if tau is None:
         tau = _TAU[D]
-    qp = _kv4_tensor(cache, q, "q", None, q.shape)
+    qp = _kv4_tensor(cache, q, "q", q.dtype, q.shape)
     if (kv_idx is None) != (kv_cnt is None):
         raise ValueError("kv_idx and kv_cnt go together")
-    max_sel = 0
+    max_sel, ip, cp = 0, None, None
     if kv_idx is not None:
         rows = (n, Hq, nblocks(Lq))
         max_sel = kv_idx.shape[-1]
         ip = _kv4_tensor(cache, kv_idx, "kv_idx", torch.int32, rows + (max_sel,))
         cp = _kv4_tensor(cache, kv_cnt, "kv_cnt", torch.int32, rows)
-    else:
-        ip = cp = None
     need = lib.sparstar_kv4_attn_work_bytes(n, Hq, cache.Hkv, Lq, D, dt)
     if need < 0:
         raise SparstarError(EDTYPE if dt < 0 else EINVAL, "sparstar_kv4_attn")
     with _Kv4Call(cache, stream) as s:
+        op = lp = None
         if out is None:
-            out = _kv4_new(s, q.shape, q.dtype, cache.device)
+            out = torch.empty_like(q)
+            op = out.data_ptr()
         if lse is None and want_lse:
-            lse = _kv4_new(s, (n, Hq, Lq), torch.float32, cache.device)
-        if work is None and need:
-            work = _kv4_new(s, (need,), torch.uint8, cache.device)
-        elif work is not None:
-            _dev(work, "work", torch.uint8)
-            if work.device != cache.device:
-                raise ValueError("work must be on %s" % cache.device)
+            lse = torch.empty(n, Hq, Lq, dtype=torch.float32, device=cache.device)
+            lp = lse.data_ptr()
+        if op is None:
+            op = _kv4_tensor(cache, out, "out", q.dtype, q.shape)
+        if lp is None and lse is not None:
+            lp = _kv4_tensor(cache, lse, "lse", torch.float32, (n, Hq, Lq))
+        if work is None:
+            work = cache._attn_work(need, s)
+        elif work.dtype is not torch.uint8 or work.get_device() != cache.index \
+                or not work.is_contiguous():
+            raise ValueError("work must be contiguous uint8 on %s" % cache.device)
         _check(lib.sparstar_kv4_attn(
             cache._struct, qp, dt, n, Hq, Lq, _kv4_ints(cache, seqs, "seqs", n), tau,
-            int(bool(causal)), ip, cp, max_sel,
-            _kv4_tensor(cache, out, "out", q.dtype, q.shape),
-            None if lse is None else _kv4_tensor(cache, lse, "lse", torch.float32, (n, Hq, Lq)),
-            None if work is None else work.data_ptr(), 0 if work is None else work.numel(),
-            _kv4_status(cache, status), s.cuda_stream), "sparstar_kv4_attn")
+            int(bool(causal)), ip, cp, max_sel, op, lp, work.data_ptr(), work.numel(),
+            _kv4_status(cache, status), s), "sparstar_kv4_attn")
     return out, lse
 
 

@@ -501,12 +501,16 @@ int sparstar_kv4_read(const sparstar_kv4_cache *cache, void *k, void *v, int dty
  *   out    [n,Hq,Lq,D] of `dtype` (device, written)
  *   lse    [n,Hq,Lq] fp32 (device, written), or NULL
  *   work   device scratch of work_bytes >= sparstar_kv4_attn_work_bytes(...),
- *          16-byte aligned, no initial contents; calls that may overlap on
- *          the GPU need one each
+ *          16-byte aligned.  Its first SPARSTAR_KV4_WORK_ZEROS bytes are zero
+ *          before its first use; a call leaves them zero (unless it sets
+ *          SPARSTAR_STATUS_TIMEOUT).  Calls that may overlap on the GPU need
+ *          one each, graphs that may be replayed at the same time too.
  * A row that sees no token gets out = 0 and lse = -inf; so do all rows of a
  * slot outside the cache.  List entries outside the sequence's pages are
  * skipped; both set SPARSTAR_STATUS_BAD_INDEX.
  */
+#define SPARSTAR_KV4_WORK_ZEROS 1024
+
 int sparstar_kv4_attn(const sparstar_kv4_cache *cache, const void *q, int dtype, int64_t n,
                       int64_t Hq, int64_t Lq, const int32_t *seqs, float tau, int causal,
                       const int32_t *kv_idx, const int32_t *kv_cnt, int64_t max_sel, void *out,

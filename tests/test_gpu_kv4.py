@@ -478,7 +478,7 @@ def serve_state(sp, n, Hq, Hkv, D, seed):
                 lens=torch.zeros(n, dtype=torch.int32, device="cuda"),
                 out=torch.empty(n, Hq, 1, D, dtype=BF16, device="cuda"),
                 lse=torch.empty(n, Hq, 1, device="cuda"),
-                work=torch.empty(max(need, 16), dtype=torch.uint8, device="cuda"))
+                work=torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda"))
 
 
 def test_a_serving_step_captured_into_graphs(sp):
