@@ -20,14 +20,18 @@ __device__ __forceinline__ float kv4_scale(uint32_t code) {
 __device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t x) {
     return (x << 4) + ((uint32_t)kScaleExp << 7) * 0x10001u;
 }
+// The same with 16 in a register (kv4_opaque): an integer fma, off the pipe
+// that the masks and shifts of the codes fill.
+__device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t x, uint32_t sixteen) {
+    return x * sixteen + ((uint32_t)kScaleExp << 7) * 0x10001u;
+}
 
 // Codes 2i and 2i + 1 of a word as the bf16 pair 128 + code (bf16 holds the
 // integers up to 256, so the code goes straight into the mantissa).  `magic`
-// is kMagic in a register of the caller's (kv4_magic): the mask and the magic
+// is kMagic in a register of the caller's (kv4_opaque): the mask and the magic
 // then take one lop3, where two constants would take two.
 constexpr uint32_t kMagic = 0x43004300u;
-__device__ __forceinline__ uint32_t kv4_magic() {
-    uint32_t m = kMagic;
+__device__ __forceinline__ uint32_t kv4_opaque(uint32_t m) {
     asm volatile("" : "+r"(m));
     return m;
 }

@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     constexpr int KS = D / 16;                 // k steps of S^T, channel tiles of O^T
     constexpr int kRow = D + 4;                // joined rows: conflict-free stores
     using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+    static_assert(kThreads >= kChunks, "build_line: one chunk a thread");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[kParts][kStages], empty[kParts][kStages];
     __shared__ uint64_t given[kParts], taken[kParts];  // the pair's exchange
@@ -392,37 +393,38 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         if (a.lse)
             for (int64_t k = threadIdx.x; k < rows; k += kThreads) a.lse[i * rows + k] = -INFINITY;
     }
-    // This part, [x, x1): an equal piece of the CTA's, the last ones shorter or
+    // This part: an equal piece of the CTA's, the last ones shorter or
     // empty.
     const int64_t c0 = min(share * blockIdx.x, total), c1 = min(c0 + share, total);
     const int64_t piece = ((uint32_t)(c1 - c0) + kParts - 1) / kParts;
-    int64_t x = min(c0 + piece * part, c1);
-    const int64_t x1 = min(x + piece, c1);
+    const int64_t start = min(c0 + piece * part, c1);
+    const int x1 = (int)(min(start + piece, c1) - start);  // tiles of the part
+    int x = 0;
     const int slot_id = blockIdx.x * kParts + part;
     uint8_t *ring = smem + part * kStages * kHalf;
-    const uint32_t magic = kv4_magic();
+    const uint32_t magic = kv4_opaque(kMagic), sixteen = kv4_opaque(16);
     const int tok0 = 32 * (r >> 1) + (r & 1);  // of row r, with 16 hp + 4 u, + 2 for r + 8
 
     // Tiles 32 at a time, one a lane; the next 32 are looked up ahead.
     Tile now, next;
-    auto lookup = [&](int64_t at) {
+    auto lookup = [&](int at) {
         Tile t;
         t.src = t.uid = -1;
         t.block = t.edge = 0;
-        if (at + lane < x1) t = locate<R>(c, a, p, line, at + lane);
+        if (at + lane < x1) t = locate<R>(c, a, p, line, start + at + lane);
         return t;
     };
-    int64_t base = x;
-    now = lookup(base);
-    next = lookup(base + 32);
+    int base = 0;
+    now = lookup(0);
+    next = lookup(32);
     // Copies: halves of tiles with a page, in order.
-    int64_t ix = x;       // next tile to copy
+    int ix = 0;           // next tile to copy
     int half_of = 0;      // its half: 0 keys, 1 values
     uint32_t issued = 0, used = 0;
     bool ok = true;
     auto issue = [&]() {  // one half, if there is one in reach
         while (ix < x1 && ix < base + 64) {
-            const int at = (int)(ix - base);
+            const int at = ix - base;
             const int64_t src =
                 __shfl_sync(0xffffffffu, at < 32 ? now.src : next.src, at & 31);
             if (src >= 0) {
@@ -456,7 +458,6 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     int seen[NT][2];                // tokens that rows 2 j, 2 j + 1 see
     int seen_min = 0;
     int uid = -1, started = 0;      // unit at work; it began with its first tile
-    Unit un{};
     uint32_t joined = 0;            // exchanges of the pair
     if (lane == 0 && leads) entry[2 * part] = entry[2 * part + 1] = -1;
 
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
             now = next;
             next = lookup(base + 32);
         }
-        const int at = (int)(x - base);
+        const int at = x - base;
         const int t_uid = __shfl_sync(0xffffffffu, now.uid, at);
         const bool t_has = __shfl_sync(0xffffffffu, (int)(now.src >= 0), at) != 0;
         const int t_block = __shfl_sync(0xffffffffu, now.block, at);
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         if (t_uid != uid) {  // a unit begins (the one before it has been stored)
             uid = t_uid;
             started = t_edge & 1;
-            un = unit_of<R>(c, a, p, uid);
+            const Unit un = unit_of<R>(c, a, p, uid);
             const int slot = kv4_slot(c, a.seqs, un.i);
             const int L = slot >= 0 ? kv4_len(c, slot) : 0;
             seen_min = 0x7fffffff;
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
                     for (int e = 0; e < 4; ++e) o[k][nt][e] = 0.0f;
         }
         if (t_has) {
-            while (issued < used + 2 && issued - used < kStages) issue();
+            while (issued < used + 2) issue();
             const int sk = used % kStages, sv = (used + 1) % kStages;
             const uint32_t pv = ((used + 1) / kStages) & 1u;
             const uint8_t *kp = ring + sk * kHalf, *vp = ring + sv * kHalf;
@@ -543,45 +544,55 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
             for (int hp = kPair > 1 ? member : 0; hp < (kPair > 1 ? member + 1 : 2); ++hp) {
                 float s[4][NT][4];
                 // ------------------------------------------ S^T = K q^T
+                // Two token tiles at a time: two chains of products.
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int u0 = 0; u0 < 4; u0 += 2) {
+                    uint32_t w[2][2][D / 32], sc[2][2], mi[2][2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int d = 0; d < 2; ++d)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.0f;
-                    uint32_t w[2][D / 32], sc[2], mi[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int tok = tok0 + 16 * hp + 4 * u + 2 * e;
-                        if constexpr (D == 128) {
-                            const uint4 v =
-                                *reinterpret_cast<const uint4 *>(kp + tok * 64 + j * 16);
-                            w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
-                            sc[e] = kv4_scale_pair(kp[kCodes + tok * 4 + j] * 0x10001u);
-                        } else {
-                            const uint2 v =
-                                *reinterpret_cast<const uint2 *>(kp + tok * 32 + j * 8);
-                            w[e][0] = v.x, w[e][1] = v.y;
-                            sc[e] = kv4_scale_pair(kp[kCodes + tok * 2 + (j >> 1)] * 0x10001u);
+                        for (int e = 0; e < 2; ++e) {
+                            const int tok = tok0 + 16 * hp + 4 * (u0 + d) + 2 * e;
+                            uint32_t(&v)[D / 32] = w[d][e];
+                            uint32_t code;
+                            if constexpr (D == 128) {
+                                const uint4 x4 =
+                                    *reinterpret_cast<const uint4 *>(kp + tok * 64 + j * 16);
+                                v[0] = x4.x, v[1] = x4.y, v[2] = x4.z, v[3] = x4.w;
+                                code = kp[kCodes + tok * 4 + j];
+                            } else {
+                                const uint2 x2 =
+                                    *reinterpret_cast<const uint2 *>(kp + tok * 32 + j * 8);
+                                v[0] = x2.x, v[1] = x2.y;
+                                code = kp[kCodes + tok * 2 + (j >> 1)];
+                            }
+                            sc[d][e] = kv4_scale_pair(code * 0x10001u, sixteen);
+                            mi[d][e] = kv4_minus136(sc[d][e]);
                         }
-                        mi[e] = kv4_minus136(sc[e]);
-                    }
 #pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        uint32_t f[4];
+                    for (int d = 0; d < 2; ++d)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                f[2 * h + e] = kv4_dequant(
-                                    kv4_pair128(w[e][k / 2], 2 * (k % 2) + h, magic), sc[e],
-                                    mi[e]);
+                            for (int e = 0; e < 4; ++e) s[u0 + d][nt][e] = 0.0f;
 #pragma unroll
-                        for (int t = kTerms - 1; t >= 0; --t)
+                    for (int k = 0; k < KS; ++k)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma(s[u][nt], f, q[t][nt][k][0], q[t][nt][k][1]);
-                    }
+                        for (int d = 0; d < 2; ++d) {
+                            uint32_t f[4];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    f[2 * h + e] = kv4_dequant(
+                                        kv4_pair128(w[d][e][k / 2], 2 * (k % 2) + h, magic),
+                                        sc[d][e], mi[d][e]);
+#pragma unroll
+                            for (int t = kTerms - 1; t >= 0; --t)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma(s[u0 + d][nt], f, q[t][nt][k][0], q[t][nt][k][1]);
+                        }
                 }
                 if (kPair > 1 || hp == 1) release();  // the keys
                 // --------------------------------------------- softmax
@@ -656,7 +667,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             sc[i] = kv4_scale_pair(
-                                __byte_perm(b[i / 2], 0, (i & 1) ? 0x4342 : 0x4140));
+                                __byte_perm(b[i / 2], 0, (i & 1) ? 0x4342 : 0x4140), sixteen);
                             mi[i] = kv4_minus136(sc[i]);
                         }
                     }
@@ -787,6 +798,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         }
         if (!leads) {
         } else if (started) {  // whole: straight to the output
+            const Unit un = unit_of<R>(c, a, p, uid);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -829,10 +841,8 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         uid = -1;
     }
     // Copies in flight land before anything else uses the ring.
-    while (used < issued) {
-        if (!wait_warp(&full[part][used % kStages], (used / kStages) & 1u)) ok = false;
-        ++used;
-    }
+    for (; used < issued; ++used)
+        ok = wait_warp(&full[part][used % kStages], (used / kStages) & 1u) && ok;
     if (!ok && lane == 0) kv4_flag(a.status, SPARSTAR_STATUS_TIMEOUT);
 
     // ------------------------------ the parts' partial results, unit by unit
