@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libsparstar.so")
 SOURCES = ["sparstar_api.cu", "pool.cu", "score.cu", "select.cu", "score_select.cu",
            "attn_simt.cu", "attn_sm100.cu", "forward_static.cu", "mass.cu",
            "transfer.cu", "kv4_pages.cu", "kv4_codec.cu", "kv4_attn.cu",
-           "kv4_attn_few.cu"]
+           "kv4_attn_few.cu", "kv4_attn_many.cu"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -39,6 +39,7 @@ def _deps():
     yield os.path.join(INCLUDE, "sparstar.h")
     yield os.path.join(CSRC, "sparstar_internal.h")
     yield os.path.join(CSRC, "kv4.cuh")
+    yield os.path.join(CSRC, "sm100.cuh")
     yield __file__
 
 

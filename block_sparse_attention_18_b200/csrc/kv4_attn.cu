@@ -2,13 +2,32 @@
 #include "kv4.cuh"
 
 namespace sparstar {
+namespace {
 
-int64_t kv4_attn_work_bytes(int64_t, int64_t, int64_t, int64_t, int D, int) {
-    return kv4_attn_few_work_bytes(D);
+// The tcgen05 kernel multiplies 128 rows whatever it is given, the other one
+// 8 or 16.
+constexpr int64_t kManyRows = 33;
+
+bool many(const Kv4Shape &s, float tau) {
+    // tau: the kernel takes the maximum of the scores before it scales them.
+    // Rows: it counts them in 32 bits, past the last block's end.
+    const int64_t rows = kv4_attn_many_rows(s);
+    return rows >= kManyRows && rows < (1 << 30) && s.D == 128 && s.dtype == SPARSTAR_BF16 &&
+           tau > 1e-30f;
 }
 
-cudaError_t launch_kv4_attn(const Kv4 &c, const Kv4Attn &a, int dtype, cudaStream_t stream) {
-    return launch_kv4_attn_few(c, a, dtype, stream);
+}  // namespace
+
+int64_t kv4_attn_work_bytes(const Kv4Shape &s) {
+    const int64_t few = kv4_attn_few_work_bytes(s.D);
+    const int64_t m = many(s, 1.0f) ? kv4_attn_many_work_bytes(s) : 0;
+    return m > few ? m : few;
+}
+
+cudaError_t launch_kv4_attn(const Kv4 &c, const Kv4Attn &a, const Kv4Shape &s,
+                            cudaStream_t stream) {
+    if (many(s, a.tau)) return launch_kv4_attn_many(c, a, s, stream);
+    return launch_kv4_attn_few(c, a, s.dtype, stream);
 }
 
 }  // namespace sparstar

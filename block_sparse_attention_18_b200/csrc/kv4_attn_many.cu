@@ -1,0 +1,989 @@
+// Attention of many query rows over the paged 4-bit key/value cache, bf16
+// with head dim 128, on the 5th-generation tensor cores.
+//
+// The pipeline is attn_sm100.cu's: one CTA a pair of query blocks A and B
+// (128 rows each), whose scores share one TMEM buffer in turn, with P in
+// tensor memory as the A operand of O += P V.  What differs is where the
+// 128 x 128 tiles come from, in one of two ways:
+//
+//   unpacked first: a kernel of its own dequantises every page once (exactly,
+//     to bf16) into scratch, as the 32 KB tiles in the 128-byte swizzle that
+//     the MMAs read from shared memory, and the attention kernel's producer
+//     fetches them with one bulk copy each.  64 KB a page and head are
+//     written and, mostly from L2, read again: right where many query blocks
+//     read the same pages.
+//   unpacked in place: three warps of the attention kernel read the packed
+//     pages into registers (the next tile's words and the page of the one
+//     after are on their way while this one is unpacked), dequantise them and
+//     write them to the ring.  Only the packed bytes cross HBM: right for few
+//     query blocks and long caches.  One warp issues both products, polling
+//     for whichever is ready, so that twelve warps keep 168 registers each (a
+//     row of scores stays in registers).
+//
+// Values lie channel by channel in a page, so both operands are K-major.
+// Without block lists A and B are neighbouring blocks of the rows that share
+// a key head (the heads of a group lie one behind the other in q) and walk
+// the same pages: a tile serves 256 rows.  With lists each block walks its
+// own.  A stripe of one block runs as both A and B, each on half of the pages
+// (one block alone would wait for its own softmax).  Few CTAs (short stripes,
+// long caches) split the pages among several; a kernel of its own joins the
+// results, in order.
+#include "kv4.cuh"
+#include "sm100.cuh"
+
+namespace sparstar {
+namespace {
+
+constexpr int kSoftmaxThreads = 256;  // warps 0-3 block A, 4-7 block B
+// Unpacked first: warp 8 copies, 9 issues S = Q K^T, 10 O += P V.  Unpacked
+// in place: warps 8-10 unpack, 11 issues both.
+template <bool kPre>
+constexpr int kThreads = kPre ? 352 : 384;
+template <bool kPre>
+constexpr int kLoadWarp = kPre ? 8 : 11;   // Q, barriers
+template <bool kPre>
+constexpr int kMmaWarp = kPre ? 9 : 11;    // TMEM, S = Q K^T
+constexpr int kPvWarp = 10, kUnpackWarp = 8, kUnpackWarps = 3;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;
+__host__ __device__ constexpr uint32_t col_p(int x) { return x ? 192u : 128u; }
+__host__ __device__ constexpr uint32_t col_o(int x) { return x ? 384u : 256u; }
+
+constexpr int kOffQ = 0;
+constexpr int kOffStage = 2 * kTileBytes;
+constexpr int kOffBar = kOffStage + kStages * kTileBytes;
+struct Bars {
+    uint64_t q_full;
+    uint64_t st_full[kStages][2];  // [stage][use & 1], see ring_parity
+    uint64_t st_empty[kStages];
+    uint64_t s_full[2];
+    uint64_t s_free;
+    uint64_t p_full[2][2];
+    uint64_t pv_done[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    int32_t n_valid[2];
+};
+constexpr int kSmemBytes = kOffBar + (int)sizeof(Bars) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+constexpr uint32_t kIdesc = make_idesc(false);  // both operands K-major
+
+// Partial results of a CTA's 256 rows: maxima, sums, accumulators.
+constexpr int kPartRows = 2 * kBlock;
+constexpr int kPartFloats = kPartRows * (kHD + 2);
+constexpr int kMaxParts = 4 * 148;  // units x splits, bounds the scratch
+constexpr int kMaxSplits = 16;
+
+struct Plan {
+    int heads;      // query heads a key head
+    int rows;       // rows of a stripe
+    int pairs;      // query block pairs of a stripe
+    int nqb;        // query blocks of a stripe
+    int splits;
+    bool halved;    // one query block a stripe: A and B are halves of its pages
+    bool joins;     // results go to `parts`
+    float sc;       // tau in log2 units, positive
+    float *parts;
+    uint8_t *tiles;  // unpacked first: [sequence][block][head] pairs of tiles
+    int tile_blocks;
+};
+constexpr int kPairBytes = 2 * kTileBytes;  // a page's keys, then its values
+
+// Whether the phase is complete, without the wait of mbar_test's try_wait.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void softmax_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+}
+
+// The pages one query block walks.
+struct Walk {
+    const int32_t *list;   // block list, or null: every block
+    const int32_t *table;  // the sequence's pages
+    int lo, hi;            // entries of this CTA
+    int blocks;            // blocks of the sequence
+    int visible;           // blocks that some row of the query block sees
+    int n_pages;
+    // The block of an entry and its page; false for one that is skipped.
+    __device__ bool at(int t, int &block, int &page) const {
+        block = list ? __ldg(list + t) : t;
+        if (block < 0 || block >= blocks || block >= visible) return false;
+        page = __ldg(table + block);
+        return page >= 0 && page < n_pages;
+    }
+    __device__ int next(int &cur, int &page) const {
+        int block = 0;
+        while (cur < hi)
+            if (at(cur++, block, page)) return block;
+        page = 0;
+        return 0;  // past the last: callers count first
+    }
+};
+
+// Rows of a tile that a lane unpacks: 16 bytes of codes (32 columns from
+// 32 g) of row q of strips of eight rows.  The four words go to four of the
+// eight 16-byte columns of the row's 128-byte line in the tile's panel; lanes
+// of the second panel take words 2, 3, 0, 1, so that the eight lanes of a
+// store phase hit eight different columns.
+struct Unpack {
+    uint32_t off[4];  // byte of word i of strip 0
+    uint32_t turn;
+    uint32_t magic, sixteen;
+    __device__ explicit Unpack(int lane) {
+        const int g = lane & 3, q = lane >> 2;
+        turn = g & 2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            off[i] = (uint32_t)((g >> 1) * kPanelBytes + q * 128 +
+                                ((((g & 1) * 4 + (i ^ (int)turn)) ^ q) << 4));
+        magic = kv4_opaque(kMagic), sixteen = kv4_opaque(16);
+    }
+    // One row's 32 keys: put(byte in the tile, 16 bytes).
+    template <typename Put>
+    __device__ void keys(const uint4 &code, uint32_t scale, int strip, Put put) const {
+        const uint32_t s = kv4_scale_pair(scale * 0x10001u, sixteen), m = kv4_minus136(s);
+        const uint32_t w[4] = {turn ? code.z : code.x, turn ? code.w : code.y,
+                               turn ? code.x : code.z, turn ? code.y : code.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = kv4_dequant(kv4_pair128(w[i], k, magic), s, m);
+            put(off[i] + strip * 1024, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+    }
+    // Scales of the 32 tokens of the lane's columns, in pairs: 16, ready.
+    struct Pairs {
+        uint32_t s[16], m[16];
+    };
+    __device__ void pairs(const uint4 &b0, const uint4 &b1, Pairs &p) const {
+        const uint32_t b[8] = {turn ? b1.x : b0.x, turn ? b1.y : b0.y, turn ? b1.z : b0.z,
+                               turn ? b1.w : b0.w, turn ? b0.x : b1.x, turn ? b0.y : b1.y,
+                               turn ? b0.z : b1.z, turn ? b0.w : b1.w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            p.s[i] = kv4_scale_pair(__byte_perm(b[i / 2], 0, (i & 1) ? 0x4342 : 0x4140), sixteen);
+            p.m[i] = kv4_minus136(p.s[i]);
+        }
+    }
+    // One channel's 32 values.
+    template <typename Put>
+    __device__ void values(const uint4 &code, const Pairs &p, int strip, Put put) const {
+        const uint32_t w[4] = {turn ? code.z : code.x, turn ? code.w : code.y,
+                               turn ? code.x : code.z, turn ? code.y : code.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                o[k] = kv4_dequant(kv4_pair128(w[i], k, magic), p.s[4 * i + k], p.m[4 * i + k]);
+            put(off[i] + strip * 1024, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+    }
+};
+
+// Unpacked first: one CTA a page and head of every sequence; four warps the
+// keys, four the values, 32 rows each.
+__global__ void __launch_bounds__(256) unpack_kernel(Kv4 c, Kv4Attn a, Plan p) {
+    const int kh = blockIdx.x % c.Hkv;
+    const int block = blockIdx.x / c.Hkv % p.tile_blocks, seq = blockIdx.x / c.Hkv / p.tile_blocks;
+    const int slot = kv4_slot(c, a.seqs, seq);
+    if (slot < 0 || block * kBlock >= kv4_len(c, slot)) return;
+    const int page = __ldg(c.table + (int64_t)slot * c.max_pages + block);
+    if (page < 0 || page >= c.n_pages) return;  // the attention kernel says so
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp & 3;
+    const int g = lane & 3, q = lane >> 2;
+    const bool values = warp >= 4;
+    const uint8_t *half = c.pages + ((int64_t)page * c.Hkv + kh) * kv4_page_bytes(kHD) +
+                          (values ? kv4_half_bytes(kHD) : 0);
+    const uint8_t *s = half + kv4_code_bytes(kHD);
+    uint4 code[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        code[i] = __ldg(reinterpret_cast<const uint4 *>(half) + (32 * w + 8 * i + q) * 4 + g);
+    uint8_t *tile = p.tiles + (int64_t)blockIdx.x * kPairBytes + (values ? kTileBytes : 0);
+    auto put = [&](uint32_t at, const uint4 &v) { *reinterpret_cast<uint4 *>(tile + at) = v; };
+    const Unpack u(lane);
+    if (values) {
+        Unpack::Pairs pairs;
+        const uint4 *sv = reinterpret_cast<const uint4 *>(s + w * kBlock + 32 * g);
+        u.pairs(__ldg(sv), __ldg(sv + 1), pairs);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u.values(code[i], pairs, 4 * w + i, put);
+    } else {
+        uint32_t scale[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scale[i] = __ldg(s + (32 * w + 8 * i + q) * 4 + g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u.keys(code[i], scale[i], 4 * w + i, put);
+    }
+}
+
+template <bool kPre>
+__global__ void __launch_bounds__(kThreads<kPre>, 1)
+    many_kernel(const __grid_constant__ CUtensorMap tmQ, Kv4 c, Kv4Attn a, Plan p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw_addr);
+    Bars *bars = reinterpret_cast<Bars *>(smem + kOffBar);
+    volatile int32_t *abort_flag = &bars->abort_flag;
+    int32_t *status = a.status;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+    // This CTA's pair of query blocks and part of their pages.  The last
+    // blocks of a stripe see most under a causal mask: they start first.
+    const int split = blockIdx.x % p.splits;
+    const int unit = blockIdx.x / p.splits;
+    const int stripe = unit / p.pairs;
+    const int qb0 = 2 * (p.pairs - 1 - unit % p.pairs);
+    const int step_b = p.halved ? 0 : 1;  // block B is qb0 + step_b
+    const bool lists = a.kv_cnt != nullptr;
+    const int per_seq = lists ? a.Hq : c.Hkv;
+    const int seq = stripe / per_seq;
+    const int kh = lists ? stripe % per_seq / p.heads : stripe % per_seq;
+    const int slot = kv4_slot(c, a.seqs, seq);
+    const int L = slot >= 0 ? kv4_len(c, slot) : 0;
+    if (slot < 0 && threadIdx.x == 0) kv4_flag(status, SPARSTAR_STATUS_BAD_INDEX);
+
+    Walk walk[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        Walk &w = walk[x];
+        const int first = (qb0 + x * step_b) * kBlock;
+        const int last = min(first + kBlock, p.rows) - 1;
+        w.list = nullptr;
+        w.table = c.table + (int64_t)(slot >= 0 ? slot : 0) * c.max_pages;
+        w.blocks = (L + kBlock - 1) / kBlock;
+        w.n_pages = c.n_pages;
+        int seen = L;  // by the row that sees most
+        if (a.causal) {
+            const int in = first % a.Lq + last - first;
+            seen = L - a.Lq + 1 + (in >= a.Lq ? a.Lq - 1 : in);
+        }
+        w.visible = last < first || seen <= 0 ? 0 : (seen + kBlock - 1) / kBlock;
+        int cnt = w.visible;
+        if (lists) {
+            cnt = 0;
+            if (last >= first) {
+                const int64_t row = (int64_t)stripe * p.nqb + qb0 + x * step_b;
+                w.list = a.kv_idx + row * a.max_sel;
+                cnt = __ldg(a.kv_cnt + row);
+                cnt = cnt < 0 || slot < 0 ? 0 : (cnt > a.max_sel ? a.max_sel : cnt);
+            }
+        }
+        w.lo = 0, w.hi = cnt;
+    }
+    {
+        // Shares of the pages; A and B cut alike where they share tiles.
+        const int most = max(walk[0].hi, walk[1].hi);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int all = lists ? walk[x].hi : most;
+            const int of = p.halved ? 2 * p.splits : p.splits;
+            const int k = p.halved ? 2 * split + x : split;
+            const int lo = (int)((int64_t)all * k / of);
+            const int hi = (int)((int64_t)all * (k + 1) / of);
+            walk[x].hi = max(lo, min(hi, walk[x].hi));
+            walk[x].lo = lo;
+        }
+    }
+
+    const uint32_t bar_q = smem_addr(&bars->q_full);
+    auto bar_full = [&](int e) {
+        return smem_addr(&bars->st_full[e % kStages][(e / kStages) & 1]);
+    };
+    auto bar_empty = [&](int s) { return smem_addr(&bars->st_empty[s]); };
+    auto bar_s = [&](int x) { return smem_addr(&bars->s_full[x]); };
+    const uint32_t bar_sfree = smem_addr(&bars->s_free);
+    auto bar_p = [&](int x, int h) { return smem_addr(&bars->p_full[x][h]); };
+    auto bar_pv = [&](int x) { return smem_addr(&bars->pv_done[x]); };
+    const uint32_t bar_drain = smem_addr(&bars->drain);
+
+    if (warp == kLoadWarp<kPre>) {
+        if (lane == 0) {
+            mbar_init(bar_q, 1);
+            for (int s = 0; s < kStages; ++s) {
+                mbar_init(smem_addr(&bars->st_full[s][0]), kPre ? 1 : kUnpackWarps);
+                mbar_init(smem_addr(&bars->st_full[s][1]), kPre ? 1 : kUnpackWarps);
+                mbar_init(bar_empty(s), 1);
+            }
+            mbar_init(bar_sfree, kSoftmaxThreads / 2);
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(bar_s(x), 1);
+                for (int h = 0; h < 2; ++h) mbar_init(bar_p(x, h), kSoftmaxThreads / 2);
+                mbar_init(bar_pv(x), 1);
+            }
+            mbar_init(bar_drain, kPre ? 2 : 1);
+            bars->abort_flag = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            int nv = 0;
+            bool bad = false;
+            for (int t = walk[x].lo + lane; t < walk[x].hi; t += 32) {
+                int block, page;
+                const bool v = walk[x].at(t, block, page);
+                nv += (int)v;
+                // A listed block that no row sees is no error.
+                bad |= !v && !(block >= walk[x].visible && block < walk[x].blocks);
+            }
+            if (bad) kv4_flag(status, SPARSTAR_STATUS_BAD_INDEX);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) nv += __shfl_xor_sync(0xffffffffu, nv, o);
+            if (lane == 0) bars->n_valid[x] = nv;
+        }
+    }
+    if (warp == kMmaWarp<kPre>) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(&bars->tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    const int nA = bars->n_valid[0], nB = bars->n_valid[1];
+    const int nmax = nA > nB ? nA : nB;
+    // Ring streams: the tiles of A and of B, or one stream for both.
+    const bool apart = lists || p.halved;
+    const int sA = apart ? nA : nmax, sB = apart ? nB : 0;
+    auto k_slot = [&](int x, int j) { return slot_k(apart ? x : 0, j, sA, sB); };
+    auto v_slot = [&](int x, int j) { return slot_v(apart ? x : 0, j, sA, sB); };
+
+    // The stream whose pages A and B share is the longer one.
+    const Walk wa = apart || nA >= nB ? walk[0] : walk[1], wb = walk[1];
+    // Tiles in ring order: bit 0 values, bit 1 stream B; -1 after the last.
+    int step = -1, phase = 0;
+    auto next_tile = [&]() {
+        while (true) {
+            if (step < 0) {
+                const int ph = phase++;
+                if (phase == 2) step = 0, phase = 0;
+                if (ph == 0 ? sA > 0 : sB > 0) return ph << 1;
+                continue;
+            }
+            if (step >= (sA > sB ? sA : sB)) return -1;
+            const int ph = phase, j = step;
+            phase = (phase + 1) & 3;
+            if (phase == 0) ++step;
+            const int n = ph < 2 ? sA : sB;
+            if (ph & 1 ? j < n : j + 1 < n) return (ph & 1) | (ph & 2);
+        }
+    };
+    int cur_k[2] = {wa.lo, wb.lo}, cur_v[2] = {wa.lo, wb.lo};
+    // The block of a tile; `page` its page.
+    auto find = [&](int tile, int &page) {
+        if (tile & 2) return wb.next(tile & 1 ? cur_v[1] : cur_k[1], page);
+        return wa.next(tile & 1 ? cur_v[0] : cur_k[0], page);
+    };
+    auto load_q = [&]() {  // by one lane
+        const uint64_t pol = policy_evict_first();
+        const int nq = nB > 0 ? 2 : 1;
+        mbar_expect_tx(bar_q, nq * kTileBytes);
+        for (int x = 0; x < nq; ++x) {
+            const uint32_t sQ = base + kOffQ + x * kTileBytes;
+            const int row = (qb0 + x * step_b) * kBlock;
+            tma_load_3d(sQ, &tmQ, bar_q, 0, row, stripe, pol);
+            tma_load_3d(sQ + kPanelBytes, &tmQ, bar_q, 64, row, stripe, pol);
+        }
+    };
+    const uint64_t dQ0 = desc_k_major(base + kOffQ);
+    const uint64_t dQ1 = desc_k_major(base + kOffQ + kTileBytes);
+    // S = Q_x K^T of ring slot e; a shared tile is free after its last reader.
+    auto issue_qk = [&](int x, int j, int e) {
+        const int stage = e % kStages;
+        const uint64_t dK = desc_k_major(base + kOffStage + stage * kTileBytes);
+        const uint64_t dQ = x == 0 ? dQ0 : dQ1;
+        const bool frees = apart || x == 1 || j >= nB;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kHD / 16; ++kk) {
+                const uint64_t o = (uint64_t)(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4);
+                mma_ss(tmem + kColS, dQ + o, dK + o, kIdesc, kk > 0 ? 1u : 0u);
+            }
+            if (frees) mma_commit(bar_empty(stage));
+            mma_commit(bar_s(x));
+        }
+        __syncwarp();
+    };
+    // O_x += P_x V over tokens 64 h .. 64 h + 63 of ring slot e.
+    auto issue_pv = [&](int x, int j, int h, int e) {
+        const int stage = e % kStages;
+        const uint64_t dV = desc_k_major(base + kOffStage + stage * kTileBytes);
+        const bool frees = apart || x == 1 || j >= nB;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+            for (int kq = 0; kq < 4; ++kq) {
+                const uint64_t o = (uint64_t)((h * kPanelBytes + kq * 32) >> 4);
+                mma_ts(tmem + col_o(x), tmem + col_p(x) + 8u * (4 * h + kq), dV + o, kIdesc,
+                       h > 0 || kq > 0 || j > 0 ? 1u : 0u);
+            }
+            if (h == 1) {
+                if (frees) mma_commit(bar_empty(stage));
+                mma_commit(bar_pv(x));
+            }
+        }
+        __syncwarp();
+    };
+
+    if (kPre && warp == kLoadWarp<kPre>) {
+        // ---------------------------------------------------- copying warp
+        if (lane == 0 && nmax > 0) {
+            load_q();
+            const uint8_t *tiles =
+                p.tiles + ((int64_t)seq * p.tile_blocks * c.Hkv + kh) * kPairBytes;
+            int e = 0, page;
+            for (int tile = next_tile(); tile >= 0; tile = next_tile()) {
+                const int block = find(tile, page);
+                const int stage = e % kStages;
+                if (!wait1(bar_empty(stage), ((uint32_t)(e / kStages) & 1u) ^ 1u, abort_flag,
+                           status))
+                    break;
+                mbar_expect_tx(bar_full(e), kTileBytes);
+                const uint8_t *src = tiles + (int64_t)block * c.Hkv * kPairBytes +
+                                     (tile & 1) * kTileBytes;
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+                    "[%1], %2, [%3];" ::"r"(base + kOffStage + stage * kTileBytes),
+                    "l"(src), "r"(kTileBytes), "r"(bar_full(e))
+                    : "memory");
+                ++e;
+            }
+            // Copies in flight land before the CTA may exit.
+            drain_wait(bar_q, 0);
+            for (int i = e > kStages ? e - kStages : 0; i < e; ++i)
+                drain_wait(bar_full(i), ring_parity(i));
+        }
+    } else if (kPre && warp == kMmaWarp<kPre>) {
+        // -------------------------------------------- S = Q K^T MMA issuer
+        bool ok = nmax > 0 && wait_warp(bar_q, 0, abort_flag, status);
+        int n = 0;
+        for (int j = 0; j < nmax && ok; ++j) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (!ok || j >= (x == 0 ? nA : nB)) continue;
+                const int e = k_slot(x, j);
+                ok = wait_warp(bar_full(e), ring_parity(e), abort_flag, status) &&
+                     (n == 0 ||
+                      wait_warp(bar_sfree, (uint32_t)(n - 1) & 1u, abort_flag, status));
+                if (!ok) break;
+                issue_qk(x, j, e);
+                ++n;
+            }
+        }
+        if (nmax > 0) {
+            if (elect_one()) mma_commit(bar_drain);
+            __syncwarp();
+        }
+    } else if (kPre && warp == kPvWarp) {
+        // ---------------------------------------------- O += P V MMA issuer
+        bool ok = nmax > 0;
+        for (int j = 0; j < nmax && ok; ++j) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (!ok || j >= (x == 0 ? nA : nB)) continue;
+                const int e = v_slot(x, j);
+                ok = wait_warp(bar_p(x, 0), (uint32_t)j & 1u, abort_flag, status) &&
+                     wait_warp(bar_full(e), ring_parity(e), abort_flag, status);
+                if (!ok) break;
+                issue_pv(x, j, 0, e);
+                ok = wait_warp(bar_p(x, 1), (uint32_t)j & 1u, abort_flag, status);
+                if (!ok) break;
+                issue_pv(x, j, 1, e);
+            }
+        }
+        if (nmax > 0) {
+            if (elect_one()) mma_commit(bar_drain);
+            __syncwarp();
+            if (lane == 0) drain_wait(bar_drain, 0);
+        }
+        __syncwarp();
+    } else if (!kPre && warp == kMmaWarp<kPre>) {
+        // ----------------------- both products, whichever is ready next
+        if (lane == 0 && nmax > 0) load_q();
+        __syncwarp();
+        bool ok = nmax > 0 && wait_warp(bar_q, 0, abort_flag, status);
+        auto ready = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_poll(bar, parity));
+        };
+        // The next S (block qx of step qj, the n-th) and the next half of O.
+        int qx = nA > 0 ? 0 : 1, qj = 0, n = 0, vx = qx, vj = 0, vh = 0;
+        auto after = [&](int &x, int &j) {  // the block after x of step j
+            do {
+                if (x == 0) x = 1;
+                else x = 0, ++j;
+            } while (j < nmax && j >= (x == 0 ? nA : nB));
+        };
+        uint64_t idle = globaltimer();
+        while (ok && (qj < nmax || vj < nmax)) {
+            bool moved = false;
+            if (qj < nmax) {
+                const int e = k_slot(qx, qj);
+                if (ready(bar_full(e), ring_parity(e)) &&
+                    (n == 0 || ready(bar_sfree, (uint32_t)(n - 1) & 1u))) {
+                    issue_qk(qx, qj, e);
+                    ++n;
+                    after(qx, qj);
+                    moved = true;
+                }
+            }
+            if (vj < nmax) {
+                const int e = v_slot(vx, vj);
+                if (ready(bar_p(vx, vh), (uint32_t)vj & 1u) &&
+                    (vh > 0 || ready(bar_full(e), ring_parity(e)))) {
+                    issue_pv(vx, vj, vh, e);
+                    vh ^= 1;
+                    if (vh == 0) after(vx, vj);
+                    moved = true;
+                }
+            }
+            if (moved) {
+                idle = globaltimer();
+            } else {
+                int give_up = 0;
+                if (lane == 0) {
+                    if (*abort_flag) {
+                        give_up = 1;
+                    } else if (globaltimer() - idle > kTimeoutNs) {
+                        *abort_flag = 1;
+                        kv4_flag(status, SPARSTAR_STATUS_TIMEOUT);
+                        give_up = 1;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, give_up, 0) == 0;
+            }
+        }
+        if (nmax > 0) {
+            if (elect_one()) mma_commit(bar_drain);
+            __syncwarp();
+            if (lane == 0) {
+                drain_wait(bar_drain, 0);
+                drain_wait(bar_q, 0);
+            }
+        }
+        __syncwarp();
+    } else if (!kPre && warp >= kUnpackWarp) {
+        // ------------------------------------------------- unpacking warps
+        // 16 strips of eight rows: 0-5, 6-10, 11-15, in two groups of channels
+        // at most (a group is four strips).
+        const int w = warp - kUnpackWarp, g = lane & 3, q = lane >> 2;
+        const int strip0 = w == 0 ? 0 : 5 * w + 1, strips = w == 0 ? 6 : 5;
+        const Unpack u(lane);
+        const int64_t head = (int64_t)kh * kv4_page_bytes(kHD);
+        const int64_t page_bytes = (int64_t)c.Hkv * kv4_page_bytes(kHD);
+        uint4 code[6], vs[2][2];
+        uint32_t ks[6];
+        auto load = [&](int tile, int page) {
+            const uint8_t *half = c.pages + page * page_bytes + head +
+                                  (tile & 1) * kv4_half_bytes(kHD);
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+                if (i < strips)
+                    code[i] = __ldg(reinterpret_cast<const uint4 *>(half) +
+                                    ((strip0 + i) * 8 + q) * 4 + g);
+            const uint8_t *s = half + kv4_code_bytes(kHD);
+            if (tile & 1) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint4 *sv = reinterpret_cast<const uint4 *>(
+                        s + ((strip0 >> 2) + k) * kBlock + 32 * g);
+                    vs[k][0] = __ldg(sv), vs[k][1] = __ldg(sv + 1);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 6; ++i)
+                    if (i < strips) ks[i] = __ldg(s + ((strip0 + i) * 8 + q) * 4 + g);
+            }
+        };
+        int e = 0, page = 0, page1 = 0, page2 = 0;
+        int tile = next_tile();
+        if (tile >= 0) {
+            find(tile, page);
+            load(tile, page);
+        }
+        int tile1 = next_tile();
+        if (tile1 >= 0) find(tile1, page1);
+        while (tile >= 0) {
+            uint4 now[6], vn[2][2];
+            uint32_t kn[6];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) now[i] = code[i], kn[i] = ks[i];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) vn[k][0] = vs[k][0], vn[k][1] = vs[k][1];
+            const int tile2 = next_tile();
+            if (tile2 >= 0) find(tile2, page2);
+            if (tile1 >= 0) load(tile1, page1);
+            const int stage = e % kStages;
+            if (!wait_warp(bar_empty(stage), ((uint32_t)(e / kStages) & 1u) ^ 1u, abort_flag,
+                           status))
+                break;
+            const uint32_t dst = base + kOffStage + stage * kTileBytes;
+            auto put = [&](uint32_t at, const uint4 &v) {
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + at),
+                             "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                             : "memory");
+            };
+            if (tile & 1) {
+                const int in_first = 4 - (strip0 & 3);  // strips of the first group
+                Unpack::Pairs pairs;
+                u.pairs(vn[0][0], vn[0][1], pairs);
+#pragma unroll
+                for (int i = 0; i < 6; ++i) {
+                    if (i == in_first) u.pairs(vn[1][0], vn[1][1], pairs);
+                    if (i < strips) u.values(now[i], pairs, strip0 + i, put);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 6; ++i)
+                    if (i < strips) u.keys(now[i], kn[i], strip0 + i, put);
+            }
+            // The MMAs read through the async proxy.
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_full(e));
+            ++e;
+            tile = tile1, tile1 = tile2, page1 = page2;
+        }
+    } else {
+        // ------------------------------- softmax + epilogue (128 per block)
+        const int x = warp >> 2;
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const uint32_t colO = col_o(x), colP = col_p(x);
+        const int nx = x == 0 ? nA : nB;
+        const float sc = p.sc;
+        const Walk wx = x == 0 ? walk[0] : walk[1];
+        const int grow = (qb0 + x * step_b) * kBlock + row;  // of the stripe
+        const bool real = grow < p.rows;
+        // Tokens the row sees; a tile is masked where a row sees part of it.
+        const int seen = a.causal ? L - a.Lq + 1 + grow % a.Lq : L;
+        const bool plain = nx == wx.hi - wx.lo;  // every entry counts
+        float m_ref = -INFINITY, l = 0.0f;
+        bool ok = true;
+        int cur = wx.lo;
+        for (int j = 0; j < nx; ++j) {
+            int kb, page;
+            if (plain) kb = wx.list ? __ldg(wx.list + wx.lo + j) : wx.lo + j;
+            else kb = wx.next(cur, page);
+            if (!wait_warp(bar_s(x), (uint32_t)j & 1u, abort_flag, status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float s[128];
+            {
+                uint32_t r[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld32(tmem + lane_base + kColS + 32 * q, r[q]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) reg_fence(r[q]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) s[32 * q + u] = __uint_as_float(r[q][u]);
+            }
+            tc_fence_before();
+            mbar_arrive(bar_sfree);
+            const int valid = seen - kb * kBlock;
+            if (__any_sync(0xffffffffu, valid < kBlock)) {
+#pragma unroll
+                for (int q = 0; q < kBlock; ++q)
+                    if (q >= valid) s[q] = -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int q = 4; q + 8 <= kBlock; q += 8) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) mx[t] = max3f(mx[t], s[q + t], s[q + 4 + t]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) mx[t] = fmaxf(mx[t], s[kBlock - 4 + t]);
+            const float m_tile = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * sc;
+            const float m_new = fmaxf(m_ref, m_tile);
+            bool pv_seen = false;
+            if (__any_sync(0xffffffffu, m_new > m_ref + 8.0f)) {
+                if (j > 0) {
+                    if (!wait_warp(bar_pv(x), (uint32_t)(j - 1) & 1u, abort_flag, status)) {
+                        ok = false;
+                break;
+                    }
+                    tc_fence_after();
+                    pv_seen = true;
+                    const float f = m_new > -INFINITY ? ex2(m_ref - m_new) : 1.0f;
+#pragma unroll 1
+                    for (int q = 0; q < kHD / 8; ++q) {
+                        uint32_t r[8];
+                        tmem_ld8(tmem + lane_base + colO + 8 * q, r);
+                        tmem_wait_ld();
+                        asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]),
+                                     "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            r[u] = __float_as_uint(__uint_as_float(r[u]) * f);
+                        tmem_st8(tmem + lane_base + colO + 8 * q, r);
+                    }
+                    tmem_wait_st();
+                }
+                if (m_new > -INFINITY) {
+                    l *= ex2(m_ref - m_new);
+                    m_ref = m_new;
+                }
+            }
+            const float neg_m = m_ref > -INFINITY ? -m_ref : 0.0f;
+            if (j > 0 && !pv_seen) {
+                if (!wait_warp(bar_pv(x), (uint32_t)(j - 1) & 1u, abort_flag, status)) {
+                    ok = false;
+                break;
+                }
+                tc_fence_after();
+            }
+            const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(neg_m, neg_m);
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t pk[64];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int u = 32 * h; u < 32 * h + 32; u += 2) {
+                    const int q = 2 * u;
+                    const float2 x01 = __ffma2_rn(make_float2(s[q], s[q + 1]), sc2, nm2);
+                    const float2 x23 = __ffma2_rn(make_float2(s[q + 2], s[q + 3]), sc2, nm2);
+                    const float2 p01 = make_float2(ex2(x01.x), ex2(x01.y));
+                    const float2 p23 = make_float2(ex2(x23.x), ex2(x23.y));
+                    ls[0] += p01.x;
+                    ls[1] += p01.y;
+                    ls[2] += p23.x;
+                    ls[3] += p23.y;
+                    pk[u] = pack_bf16(p01.x, p01.y);
+                    pk[u + 1] = pack_bf16(p23.x, p23.y);
+                }
+                tmem_st32(tmem + lane_base + colP + 32 * h, pk + 32 * h);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar_p(x, h));
+            }
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        }
+
+        // ---- epilogue
+        const bool have = nx > 0 && ok &&
+                          wait_warp(bar_pv(x), (uint32_t)(nx - 1) & 1u, abort_flag, status);
+        if (have) tc_fence_after();
+        const int64_t out_row = (int64_t)stripe * p.rows + grow;
+        float *part = p.parts + (int64_t)blockIdx.x * kPartFloats;
+        float *part_o = part + 2 * kPartRows + (int64_t)(x * kBlock + row) * kHD;
+        // A row without a weight (no token seen) gets 0.
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t r[32];
+#pragma unroll
+            for (int u = 0; u < 32; ++u) r[u] = 0;
+            if (have) {
+                tmem_ld32(tmem + lane_base + colO + 32 * q, r);
+                tmem_wait_ld();
+                reg_fence(r);
+            }
+            if (!real || (nx > 0 && !have)) continue;
+            if (p.joins) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    reinterpret_cast<uint4 *>(part_o + 32 * q)[u] =
+                        make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+            } else {
+                uint4 *o4 = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                      out_row * kHD + 32 * q);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = nx == 0 ? 0u
+                                       : pack_bf16(__uint_as_float(r[8 * u + 2 * k]) * inv,
+                                                   __uint_as_float(r[8 * u + 2 * k + 1]) * inv);
+                    __stcs(o4 + u, make_uint4(v[0], v[1], v[2], v[3]));
+                }
+            }
+        }
+        if (p.joins) {
+            part[x * kBlock + row] = m_ref;
+            part[kPartRows + x * kBlock + row] = l;
+        } else if (real && a.lse && (nx == 0 || have)) {
+            a.lse[out_row] = (m_ref + log2f(l)) * 0.6931471805599453f;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp<kPre>) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols)
+                     : "memory");
+    }
+}
+
+// Joins the parts of every row, in order: a warp a row, four channels a lane.
+// All maxima and sums at once (one a lane), then eight accumulators a step.
+__global__ void __launch_bounds__(256) many_join_kernel(Kv4Attn a, Plan p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = p.halved ? kBlock : kPartRows;  // of a unit
+    const int unit = blockIdx.x / (rows / 8), r0 = blockIdx.x % (rows / 8) * 8 + warp;
+    const int stripe = unit / p.pairs;
+    const int srow = 2 * (p.pairs - 1 - unit % p.pairs) * kBlock + r0;
+    if (srow >= p.rows) return;
+    const int n = p.halved ? 2 * p.splits : p.splits;  // <= 32
+    const float *first = p.parts + (int64_t)unit * p.splits * kPartFloats;
+    auto row_of = [&](int k, int &row) {  // record and row of part k
+        row = p.halved ? (k & 1) * kBlock + r0 : r0;
+        return first + (int64_t)(p.halved ? k >> 1 : k) * kPartFloats;
+    };
+    float m = -INFINITY, l = 0.0f;
+    if (lane < n) {
+        int row;
+        const float *rec = row_of(lane, row);
+        m = rec[row], l = rec[kPartRows + row];
+    }
+    float top = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = m > -INFINITY ? ex2(m - top) : 0.0f;
+    float sum = f * l;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < n; k0 += 8) {
+        float4 x[8];
+        float w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            w[k] = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            int row;
+            const float *rec = row_of(k0 + k, row);
+            // Parts without a seen token have stored nothing.
+            if (k0 + k < n && w[k] != 0.0f)
+                x[k] = *(reinterpret_cast<const float4 *>(rec + 2 * kPartRows + row * kHD) + lane);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            acc.x = fmaf(w[k], x[k].x, acc.x), acc.y = fmaf(w[k], x[k].y, acc.y);
+            acc.z = fmaf(w[k], x[k].z, acc.z), acc.w = fmaf(w[k], x[k].w, acc.w);
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t out_row = (int64_t)stripe * p.rows + srow;
+    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * kHD)[lane] =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (lane == 0 && a.lse) a.lse[out_row] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Stripes and pairs of query blocks of a call.
+struct Shape {
+    int64_t stripes, rows, pairs;
+    int64_t units() const { return stripes * pairs; }
+    bool halved() const { return rows <= kBlock; }
+};
+Shape shape_of(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq, bool lists) {
+    Shape s;
+    s.stripes = n * (lists ? Hq : Hkv);
+    s.rows = lists ? Lq : Hq / Hkv * Lq;
+    s.pairs = ceil_div(s.rows, kPartRows);
+    return s;
+}
+
+// Splits of a unit's pages: the number that makes the waves of CTAs shortest,
+// in tiles; a wave costs about four tiles beside its own, a split's joining
+// about one more.
+int splits_of(int64_t units, int64_t tiles) {
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= kMaxSplits; ++s) {
+        if (s > 1 && (units * s > kMaxParts || tiles < 2 * s)) break;
+        const double waves = (double)ceil_div(units * s, 148);
+        const double cost = waves * ((double)tiles / s + 4.0) + (s > 1 ? 3.0 + s : 0.0);
+        if (s == 1 || cost < least) best = s, least = cost;
+    }
+    return best;
+}
+
+// Scratch of the splits of a call, whatever their number.
+int64_t part_bytes(const Shape &s) {
+    const int64_t u = s.units();
+    if (2 * u > kMaxParts) return s.halved() ? u * kPartFloats * 4 : 0;
+    const int64_t most = kMaxParts / u < kMaxSplits ? kMaxParts / u : kMaxSplits;
+    return u * most * kPartFloats * 4;
+}
+
+// Whether the pages are unpacked first.  That costs 22 ns a page and head
+// (measured, over the whole GPU); unpacking in place makes a visit of a page
+// by a pair of blocks 9 ns longer, by a block with its own list 12 ns.
+bool unpack_first(const Shape &s, const Kv4Shape &k) {
+    if (k.n * k.max_pages * k.Hkv * kPairBytes > ((int64_t)2 << 30)) return false;
+    if (!k.lists) return s.pairs >= 3;
+    return (double)(k.Hq / k.Hkv) * (double)ceil_div(s.rows, kBlock) * (double)k.max_sel >
+           2.0 * (double)k.max_pages;
+}
+
+}  // namespace
+
+int64_t kv4_attn_many_rows(const Kv4Shape &k) {
+    return shape_of(k.n, k.Hq, k.Hkv, k.Lq, k.lists).rows;
+}
+
+int64_t kv4_attn_many_work_bytes(const Kv4Shape &k) {
+    const Shape s = shape_of(k.n, k.Hq, k.Hkv, k.Lq, k.lists);
+    return SPARSTAR_KV4_WORK_ZEROS + part_bytes(s) +
+           (unpack_first(s, k) ? k.n * k.max_pages * k.Hkv * kPairBytes : 0);
+}
+
+cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape &k,
+                                 cudaStream_t stream) {
+    const Shape s = shape_of(k.n, k.Hq, k.Hkv, k.Lq, k.lists);
+    CUtensorMap mq;
+    if (!encode(&mq, a.q, s.stripes, s.rows)) return cudaErrorUnknown;
+    Plan p;
+    p.heads = a.Hq / c.Hkv;
+    p.rows = (int)s.rows;
+    p.pairs = (int)s.pairs;
+    p.nqb = (int)ceil_div(s.rows, kBlock);
+    p.splits = splits_of(s.units(), k.lists ? a.max_sel : c.max_pages);
+    p.sc = a.tau * 1.4426950408889634f;
+    p.halved = s.halved();
+    p.joins = p.halved || p.splits > 1;
+    p.parts = static_cast<float *>(a.work) + SPARSTAR_KV4_WORK_ZEROS / 4;
+    p.tiles = static_cast<uint8_t *>(a.work) + SPARSTAR_KV4_WORK_ZEROS + part_bytes(s);
+    p.tile_blocks = c.max_pages;
+    const bool first = unpack_first(s, k);
+    const auto kernel = first ? many_kernel<true> : many_kernel<false>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (first)
+        unpack_kernel<<<(unsigned)((int64_t)a.n * c.max_pages * c.Hkv), 256, 0, stream>>>(c, a, p);
+    kernel<<<(unsigned)(s.units() * p.splits), first ? kThreads<true> : kThreads<false>,
+             kSmemBytes, stream>>>(mq, c, a, p);
+    if (p.joins)
+        many_join_kernel<<<(unsigned)(s.units() * (p.halved ? kBlock : kPartRows) / 8), 256, 0,
+                           stream>>>(a, p);
+    return cudaGetLastError();
+}
+
+}  // namespace sparstar

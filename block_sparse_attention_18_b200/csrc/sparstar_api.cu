@@ -463,12 +463,26 @@ SPARSTAR_API int sparstar_kv4_read(const sparstar_kv4_cache *cache, void *k, voi
                                                  status, static_cast<cudaStream_t>(stream)));
 }
 
-SPARSTAR_API int64_t sparstar_kv4_attn_work_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq,
-                                                  int64_t D, int dtype) {
+namespace {
+
+bool kv4_shape(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq, int64_t D, int dtype,
+               int64_t max_pages, int64_t max_sel, sparstar::Kv4Shape *s) {
     if (n < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq > 65535 || Lq < 1 || Lq > kMaxTokens ||
-        !head_dim_ok(D) || !dtype_ok(dtype) || n > kMaxGrid / Hq || n * Hq > kMaxGrid / Lq)
-        return -1;
-    return sparstar::kv4_attn_work_bytes(n, Hq, Hkv, Lq, (int)D, dtype);
+        !head_dim_ok(D) || !dtype_ok(dtype) || max_pages < 1 || max_pages > (1 << 23) ||
+        n > kMaxGrid / Hq || n * Hq > kMaxGrid / Lq || max_sel < -1 || max_sel > 0x7fffffffLL)
+        return false;
+    *s = sparstar::Kv4Shape{n, Hq, Hkv, Lq, max_pages, (int)D, dtype, max_sel >= 0, max_sel};
+    return true;
+}
+
+}  // namespace
+
+SPARSTAR_API int64_t sparstar_kv4_attn_work_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq,
+                                                  int64_t D, int dtype, int64_t max_pages,
+                                                  int64_t max_sel) {
+    sparstar::Kv4Shape s;
+    if (!kv4_shape(n, Hq, Hkv, Lq, D, dtype, max_pages, max_sel, &s)) return -1;
+    return sparstar::kv4_attn_work_bytes(s);
 }
 
 SPARSTAR_API int sparstar_kv4_attn(const sparstar_kv4_cache *cache, const void *q, int dtype,
@@ -491,16 +505,17 @@ SPARSTAR_API int sparstar_kv4_attn(const sparstar_kv4_cache *cache, const void *
         !aligned4(kv_idx) || !aligned4(kv_cnt) || !aligned4(lse))
         return SPARSTAR_EINVAL;
     // One list entry names one of n_seqs slots, or several entries the same.
-    const int64_t need = sparstar_kv4_attn_work_bytes(n, Hq, c.Hkv, Lq, c.D, dtype);
-    if (need < 0 || (!seqs && n > c.n_seqs)) return SPARSTAR_EINVAL;
-    if (work_bytes < need) return SPARSTAR_ESIZE;
-    if (need > 0 && !work) return SPARSTAR_EINVAL;
+    sparstar::Kv4Shape s;
+    if (!kv4_shape(n, Hq, c.Hkv, Lq, c.D, dtype, c.max_pages, kv_cnt ? max_sel : -1, &s) ||
+        (!seqs && n > c.n_seqs) || !work)
+        return SPARSTAR_EINVAL;
+    if (work_bytes < sparstar::kv4_attn_work_bytes(s)) return SPARSTAR_ESIZE;
     if (int rc = device_check()) return rc;
     const sparstar::Kv4Attn a{q,      (int32_t)n, (int32_t)Hq,      (int32_t)Lq, causal, seqs,
                               tau,    kv_idx,     kv_cnt,           (int32_t)max_sel,
                               out,    lse,        work,             status};
     return cuda_status(
-        sparstar::launch_kv4_attn(c, a, dtype, static_cast<cudaStream_t>(stream)));
+        sparstar::launch_kv4_attn(c, a, s, static_cast<cudaStream_t>(stream)));
 }
 
 SPARSTAR_API int sparstar_test_attn_timeout(const void *q, const void *k, const void *v,

@@ -124,9 +124,22 @@ struct Kv4Attn {
     void *work;
     int32_t *status;
 };
-cudaError_t launch_kv4_attn(const Kv4 &c, const Kv4Attn &a, int dtype, cudaStream_t stream);
+// The sizes that decide which kernel takes a call and how much scratch.
+struct Kv4Shape {
+    int64_t n, Hq, Hkv, Lq, max_pages;
+    int D, dtype;
+    bool lists;
+    int64_t max_sel;  // with lists
+};
+cudaError_t launch_kv4_attn(const Kv4 &c, const Kv4Attn &a, const Kv4Shape &s,
+                            cudaStream_t stream);
+int64_t kv4_attn_work_bytes(const Kv4Shape &s);
 cudaError_t launch_kv4_attn_few(const Kv4 &c, const Kv4Attn &a, int dtype, cudaStream_t stream);
 int64_t kv4_attn_few_work_bytes(int D);
-int64_t kv4_attn_work_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq, int D, int dtype);
+// bf16, D = 128, tau > 0; rows: of a stripe (see kv4_attn_many.cu)
+cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape &s,
+                                 cudaStream_t stream);
+int64_t kv4_attn_many_work_bytes(const Kv4Shape &s);
+int64_t kv4_attn_many_rows(const Kv4Shape &s);
 
 }  // namespace sparstar

@@ -83,7 +83,7 @@ def _load():
     L.sparstar_kv4_read.argtypes = [kv4, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp]
     L.sparstar_kv4_attn.argtypes = [kv4, vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, i64, vp,
                                     vp, vp, i64, vp, vp]
-    L.sparstar_kv4_attn_work_bytes.argtypes = [i64, i64, i64, i64, i64, i32]
+    L.sparstar_kv4_attn_work_bytes.argtypes = [i64, i64, i64, i64, i64, i32, i64, i64]
     L.sparstar_kv4_attn_work_bytes.restype = i64
     for name in ("sparstar_kv4_resize", "sparstar_kv4_fork", "sparstar_kv4_compact",
                  "sparstar_kv4_write", "sparstar_kv4_read", "sparstar_kv4_attn"):
@@ -619,9 +619,11 @@ def sparstar_kv4_read(cache: Kv4Cache, T: int, n: int = None, dtype=torch.bfloat
     return k, v
 
 
-def sparstar_kv4_attn_work_bytes(n: int, Hq: int, Hkv: int, Lq: int, D: int,
-                                 dtype=torch.bfloat16) -> int:
-    return lib.sparstar_kv4_attn_work_bytes(n, Hq, Hkv, Lq, D, _DTYPE.get(dtype, -1))
+def sparstar_kv4_attn_work_bytes(n: int, Hq: int, Hkv: int, Lq: int, D: int, max_pages: int,
+                                 dtype=torch.bfloat16, max_sel: int = -1) -> int:
+    """Bytes of scratch; max_sel: row stride of the block lists, -1 without."""
+    return lib.sparstar_kv4_attn_work_bytes(n, Hq, Hkv, Lq, D, _DTYPE.get(dtype, -1), max_pages,
+                                            max_sel)
 
 
 def sparstar_kv4_attn(cache: Kv4Cache, q, seqs=None, tau: float = None, causal: bool = False,
@@ -648,7 +650,8 @@ def sparstar_kv4_attn(cache: Kv4Cache, q, seqs=None, tau: float = None, causal: 
         max_sel = kv_idx.shape[-1]
         ip = _kv4_tensor(cache, kv_idx, "kv_idx", torch.int32, rows + (max_sel,))
         cp = _kv4_tensor(cache, kv_cnt, "kv_cnt", torch.int32, rows)
-    need = lib.sparstar_kv4_attn_work_bytes(n, Hq, cache.Hkv, Lq, D, dt)
+    need = lib.sparstar_kv4_attn_work_bytes(n, Hq, cache.Hkv, Lq, D, dt, cache.max_pages,
+                                            -1 if kv_idx is None else max_sel)
     if need < 0:
         raise SparstarError(EDTYPE if dt < 0 else EINVAL, "sparstar_kv4_attn")
     with _Kv4Call(cache, stream) as s:

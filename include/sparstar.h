@@ -517,9 +517,11 @@ int sparstar_kv4_attn(const sparstar_kv4_cache *cache, const void *q, int dtype,
                       float *lse, void *work, int64_t work_bytes, int32_t *status,
                       void *stream);
 
-/* Bytes of `work` (host only; 0 is possible); -1 for sizes that attn refuses. */
+/* Bytes of `work` (host only); max_sel: -1 without block lists.  -1 for
+ * sizes that attn refuses.  Many query rows with D = 128 and bf16 may use
+ * 64 KB a page and head (2 GB at most) to unpack the pages once. */
 int64_t sparstar_kv4_attn_work_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq, int64_t D,
-                                     int dtype);
+                                     int dtype, int64_t max_pages, int64_t max_sel);
 
 /*
  * sparstar_test_attn_timeout — TEST HOOK for failure detection, not part of

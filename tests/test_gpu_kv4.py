@@ -471,14 +471,14 @@ def serve_step(sp, cache, st):
     return sp.sparstar_kv4_attn(cache, st["q"], out=st["out"], lse=st["lse"], work=st["work"])
 
 
-def serve_state(sp, n, Hq, Hkv, D, seed):
+def serve_state(sp, n, Hq, Hkv, D, seed, max_pages=7):
     k, v = tokens(n, Hkv, 1, D, BF16, seed)
-    need = sp.sparstar_kv4_attn_work_bytes(n, Hq, Hkv, 1, D)
+    need = sp.sparstar_kv4_attn_work_bytes(n, Hq, Hkv, 1, D, max_pages)
     return dict(k=k, v=v, q=queries(n, Hq, 1, D, BF16, seed),
                 lens=torch.zeros(n, dtype=torch.int32, device="cuda"),
                 out=torch.empty(n, Hq, 1, D, dtype=BF16, device="cuda"),
                 lse=torch.empty(n, Hq, 1, device="cuda"),
-                work=torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda"))
+                work=torch.zeros(need, dtype=torch.uint8, device="cuda"))
 
 
 def test_a_serving_step_captured_into_graphs(sp):

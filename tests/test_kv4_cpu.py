@@ -85,9 +85,9 @@ def test_attention_refuses_bad_arguments(sp):
                dict(idx=A, sel=3), dict(cnt=A, sel=3), dict(lse=MIS), dict(seqs=MIS),
                dict(n=1 << 20, seqs=A, Lq=1 << 12)):
         assert call(**kw) == sp.EINVAL, kw
-    if sp.lib.sparstar_kv4_attn_work_bytes(1, 4, 2, 1, 128, 0) > 0:
-        assert call(bytes=15) == sp.ESIZE
-        assert call(work=0) == sp.EINVAL
+    need = sp.sparstar_kv4_attn_work_bytes(1, 4, 2, 1, 128, 16)
+    assert call(bytes=need - 1) == sp.ESIZE
+    assert call(work=0) == sp.EINVAL
 
 
 def test_sizes(sp):
@@ -96,9 +96,11 @@ def test_sizes(sp):
     assert sp.sparstar_kv4_page_bytes(96) == -1
     assert sp.lib.sparstar_kv4_work_ints(0, 1) == -1
     assert sp.lib.sparstar_kv4_work_ints(10, 3) >= 13
-    for bad in ((0, 4, 2, 1, 128), (1, 3, 2, 1, 128), (1, 4, 2, 1, 80), (1, 4, 2, 0, 128)):
+    for bad in ((0, 4, 2, 1, 128, 9), (1, 3, 2, 1, 128, 9), (1, 4, 2, 1, 80, 9),
+                (1, 4, 2, 0, 128, 9), (1, 4, 2, 1, 128, 0)):
         assert sp.sparstar_kv4_attn_work_bytes(*bad) == -1
-    assert sp.sparstar_kv4_attn_work_bytes(1, 4, 2, 1, 128, torch.float16) == -1
+    assert sp.sparstar_kv4_attn_work_bytes(1, 4, 2, 1, 128, 9, torch.float16) == -1
+    assert sp.sparstar_kv4_attn_work_bytes(1, 4, 2, 1, 128, 9) >= sp.KV4_WORK_ZEROS
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device answer")
