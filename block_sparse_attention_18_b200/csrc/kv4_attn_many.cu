@@ -74,15 +74,18 @@ constexpr int kPartRows = 2 * kBlock;
 constexpr int kPartFloats = kPartRows * (kHD + 2);
 constexpr int kMaxParts = 4 * 148;  // units x splits, bounds the scratch
 constexpr int kMaxSplits = 16;
+// Scratch: the other kernel's zeros, the chosen chunk, the parts, the tiles.
+constexpr int kHeadBytes = SPARSTAR_KV4_WORK_ZEROS + 1024;
 
 struct Plan {
     int heads;      // query heads a key head
     int rows;       // rows of a stripe
     int pairs;      // query block pairs of a stripe
     int nqb;        // query blocks of a stripe
-    int splits;
+    int splits;     // CTAs a unit; those behind its last page have nothing to do
+    int chunk;      // entries (pages or list entries) a CTA
+    int32_t *chosen;  // unpacked first, without lists: the chunk that the lengths ask for
     bool halved;    // one query block a stripe: A and B are halves of its pages
-    bool joins;     // results go to `parts`
     float sc;       // tau in log2 units, positive
     float *parts;
     uint8_t *tiles;  // unpacked first: [sequence][block][head] pairs of tiles
@@ -129,6 +132,110 @@ struct Walk {
         return 0;  // past the last: callers count first
     }
 };
+
+// A unit: a pair of query blocks of a stripe, and what they walk.
+struct Unit {
+    int stripe, qb0, seq, kh, slot, L;
+    int step_b;      // block B is qb0 + step_b
+    int visible[2];  // blocks that some row of the query block sees
+    int count[2];    // entries it walks
+    int entries, chunk, parts;
+};
+// The last blocks of a stripe see most under a causal mask: they come first.
+__device__ Unit unit_of(const Kv4 &c, const Kv4Attn &a, const Plan &p, int unit) {
+    Unit u;
+    u.stripe = unit / p.pairs;
+    u.qb0 = 2 * (p.pairs - 1 - unit % p.pairs);
+    u.step_b = p.halved ? 0 : 1;
+    const bool lists = a.kv_cnt != nullptr;
+    const int per_seq = lists ? a.Hq : c.Hkv;
+    u.seq = u.stripe / per_seq;
+    u.kh = lists ? u.stripe % per_seq / p.heads : u.stripe % per_seq;
+    u.slot = kv4_slot(c, a.seqs, u.seq);
+    u.L = u.slot >= 0 ? kv4_len(c, u.slot) : 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int first = (u.qb0 + x * u.step_b) * kBlock;
+        const int last = min(first + kBlock, p.rows) - 1;
+        int seen = u.L;  // by the row that sees most
+        if (a.causal) {
+            const int in = first % a.Lq + last - first;
+            seen = u.L - a.Lq + 1 + (in >= a.Lq ? a.Lq - 1 : in);
+        }
+        u.visible[x] = last < first || seen <= 0 ? 0 : (seen + kBlock - 1) / kBlock;
+        u.count[x] = u.visible[x];
+        if (lists) {
+            u.count[x] = 0;
+            if (last >= first && u.slot >= 0) {
+                const int cnt = __ldg(a.kv_cnt + (int64_t)u.stripe * p.nqb + first / kBlock);
+                u.count[x] = cnt < 0 ? 0 : (cnt > a.max_sel ? a.max_sel : cnt);
+            }
+        }
+    }
+    u.entries = max(u.count[0], u.count[1]);
+    u.chunk = p.chosen ? __ldcg(p.chosen) : p.chunk;
+    u.parts = max(1, (u.entries + u.chunk - 1) / u.chunk);
+    return u;
+}
+
+// The cost of a call whose units' pages are cut into chunks, in steps of a
+// pair of blocks over one page (1.9 us): a CTA takes about four steps beside
+// its pages, and four more to store 133 KB where the results are joined,
+// which reads them at 0.02 steps a CTA.  Equal CTAs run in waves; unequal
+// ones follow each other and end about half a chunk apart.
+__host__ __device__ inline float cost_of(float ctas, float chunk, float steps, bool joins,
+                                         bool equal) {
+    const float own = chunk + (joins ? 8.0f : 4.0f);
+    const float join = joins ? 3.0f + 0.02f * ctas : 0.0f;
+    if (equal) return ceilf(ctas / 148.0f) * own + join;
+    const float packed = (steps + (joins ? 8.0f : 4.0f) * ctas) / 148.0f + 0.5f * chunk;
+    return fmaxf(own, packed) + join;
+}
+
+// The chunk for the lengths at hand (no lists): of 1 .. splits chunks for the
+// longest unit, the number of least cost.  One CTA.
+__device__ void choose_chunk(const Kv4 &c, const Kv4Attn &a, const Plan &p) {
+    __shared__ int32_t longest, ctas[kMaxSplits + 1];
+    __shared__ unsigned long long steps;
+    if (threadIdx.x == 0) longest = 1, steps = 0;
+    if (threadIdx.x <= kMaxSplits) ctas[threadIdx.x] = 0;
+    __syncthreads();
+    // The key heads of a sequence have equal units: one stands for all.
+    const int units = a.n * p.pairs;
+    Plan q = p;
+    q.chosen = nullptr;
+    auto entries = [&](int k) {
+        return unit_of(c, a, q, k / p.pairs * c.Hkv * p.pairs + k % p.pairs).entries;
+    };
+    for (int k = threadIdx.x; k < units; k += blockDim.x) {
+        const int e = entries(k);
+        atomicMax(&longest, e);
+        atomicAdd(&steps, (unsigned long long)e);
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < units; k += blockDim.x) {
+        const int e = entries(k);
+        for (int s = 1; s <= p.splits; ++s) {
+            const int chunk = (longest + s - 1) / s;
+            atomicAdd(&ctas[s], max(1, (e + chunk - 1) / chunk));
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const float all = (float)steps * c.Hkv;
+        const bool equal = all >= 0.95f * (float)units * c.Hkv * longest;
+        int best = longest;
+        float least = 0.0f;
+        for (int s = 1; s <= p.splits; ++s) {
+            const int chunk = (longest + s - 1) / s;
+            if (s > 1 && chunk < 2) break;
+            const float cost =
+                cost_of((float)ctas[s] * c.Hkv, (float)chunk, all, s > 1, equal);
+            if (s == 1 || cost < least) best = chunk, least = cost;
+        }
+        *p.chosen = best;
+    }
+}
 
 // Rows of a tile that a lane unpacks: 16 bytes of codes (32 columns from
 // 32 g) of row q of strips of eight rows.  The four words go to four of the
@@ -195,6 +302,10 @@ struct Unpack {
 // Unpacked first: one CTA a page and head of every sequence; four warps the
 // keys, four the values, 32 rows each.
 __global__ void __launch_bounds__(256) unpack_kernel(Kv4 c, Kv4Attn a, Plan p) {
+    if (p.chosen && blockIdx.x == gridDim.x - 1) {  // one CTA behind the pages'
+        choose_chunk(c, a, p);
+        return;
+    }
     const int kh = blockIdx.x % c.Hkv;
     const int block = blockIdx.x / c.Hkv % p.tile_blocks, seq = blockIdx.x / c.Hkv / p.tile_blocks;
     const int slot = kv4_slot(c, a.seqs, seq);
@@ -241,61 +352,30 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
     int32_t *status = a.status;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
-    // This CTA's pair of query blocks and part of their pages.  The last
-    // blocks of a stripe see most under a causal mask: they start first.
+    // This CTA's pair of query blocks and part of their pages.
     const int split = blockIdx.x % p.splits;
-    const int unit = blockIdx.x / p.splits;
-    const int stripe = unit / p.pairs;
-    const int qb0 = 2 * (p.pairs - 1 - unit % p.pairs);
-    const int step_b = p.halved ? 0 : 1;  // block B is qb0 + step_b
+    const Unit un = unit_of(c, a, p, blockIdx.x / p.splits);
+    const int stripe = un.stripe, qb0 = un.qb0, step_b = un.step_b, L = un.L;
+    const int seq = un.seq, kh = un.kh;
     const bool lists = a.kv_cnt != nullptr;
-    const int per_seq = lists ? a.Hq : c.Hkv;
-    const int seq = stripe / per_seq;
-    const int kh = lists ? stripe % per_seq / p.heads : stripe % per_seq;
-    const int slot = kv4_slot(c, a.seqs, seq);
-    const int L = slot >= 0 ? kv4_len(c, slot) : 0;
-    if (slot < 0 && threadIdx.x == 0) kv4_flag(status, SPARSTAR_STATUS_BAD_INDEX);
-
+    if (un.slot < 0 && threadIdx.x == 0) kv4_flag(status, SPARSTAR_STATUS_BAD_INDEX);
+    if (split >= un.parts) return;
+    const bool joins = p.halved || un.parts > 1;  // the result goes to `parts`
     Walk walk[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        Walk &w = walk[x];
-        const int first = (qb0 + x * step_b) * kBlock;
-        const int last = min(first + kBlock, p.rows) - 1;
-        w.list = nullptr;
-        w.table = c.table + (int64_t)(slot >= 0 ? slot : 0) * c.max_pages;
-        w.blocks = (L + kBlock - 1) / kBlock;
-        w.n_pages = c.n_pages;
-        int seen = L;  // by the row that sees most
-        if (a.causal) {
-            const int in = first % a.Lq + last - first;
-            seen = L - a.Lq + 1 + (in >= a.Lq ? a.Lq - 1 : in);
-        }
-        w.visible = last < first || seen <= 0 ? 0 : (seen + kBlock - 1) / kBlock;
-        int cnt = w.visible;
-        if (lists) {
-            cnt = 0;
-            if (last >= first) {
-                const int64_t row = (int64_t)stripe * p.nqb + qb0 + x * step_b;
-                w.list = a.kv_idx + row * a.max_sel;
-                cnt = __ldg(a.kv_cnt + row);
-                cnt = cnt < 0 || slot < 0 ? 0 : (cnt > a.max_sel ? a.max_sel : cnt);
-            }
-        }
-        w.lo = 0, w.hi = cnt;
-    }
     {
-        // Shares of the pages; A and B cut alike where they share tiles.
-        const int most = max(walk[0].hi, walk[1].hi);
+        const int lo = split * un.chunk, hi = min(lo + un.chunk, un.entries);
+        const int mid = (lo + hi + 1) / 2;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int all = lists ? walk[x].hi : most;
-            const int of = p.halved ? 2 * p.splits : p.splits;
-            const int k = p.halved ? 2 * split + x : split;
-            const int lo = (int)((int64_t)all * k / of);
-            const int hi = (int)((int64_t)all * (k + 1) / of);
-            walk[x].hi = max(lo, min(hi, walk[x].hi));
-            walk[x].lo = lo;
+            Walk &w = walk[x];
+            w.list = lists ? a.kv_idx + ((int64_t)stripe * p.nqb + qb0 + x * step_b) * a.max_sel
+                           : nullptr;
+            w.table = c.table + (int64_t)(un.slot >= 0 ? un.slot : 0) * c.max_pages;
+            w.blocks = (L + kBlock - 1) / kBlock;
+            w.n_pages = c.n_pages;
+            w.visible = un.visible[x];
+            w.lo = p.halved && x == 1 ? mid : lo;
+            w.hi = max(w.lo, min(p.halved && x == 0 ? mid : hi, un.count[x]));
         }
     }
 
@@ -802,7 +882,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 reg_fence(r);
             }
             if (!real || (nx > 0 && !have)) continue;
-            if (p.joins) {
+            if (joins) {
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
                     reinterpret_cast<uint4 *>(part_o + 32 * q)[u] =
@@ -822,7 +902,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 }
             }
         }
-        if (p.joins) {
+        if (joins) {
             part[x * kBlock + row] = m_ref;
             part[kPartRows + x * kBlock + row] = l;
         } else if (real && a.lse && (nx == 0 || have)) {
@@ -842,14 +922,14 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
 
 // Joins the parts of every row, in order: a warp a row, four channels a lane.
 // All maxima and sums at once (one a lane), then eight accumulators a step.
-__global__ void __launch_bounds__(256) many_join_kernel(Kv4Attn a, Plan p) {
+__global__ void __launch_bounds__(256) many_join_kernel(Kv4 c, Kv4Attn a, Plan p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.halved ? kBlock : kPartRows;  // of a unit
     const int unit = blockIdx.x / (rows / 8), r0 = blockIdx.x % (rows / 8) * 8 + warp;
-    const int stripe = unit / p.pairs;
-    const int srow = 2 * (p.pairs - 1 - unit % p.pairs) * kBlock + r0;
-    if (srow >= p.rows) return;
-    const int n = p.halved ? 2 * p.splits : p.splits;  // <= 32
+    const Unit u = unit_of(c, a, p, unit);
+    const int srow = u.qb0 * kBlock + r0;
+    if (srow >= p.rows || (!p.halved && u.parts == 1)) return;
+    const int n = p.halved ? 2 * u.parts : u.parts;  // <= 32
     const float *first = p.parts + (int64_t)unit * p.splits * kPartFloats;
     auto row_of = [&](int k, int &row) {  // record and row of part k
         row = p.halved ? (k & 1) * kBlock + r0 : r0;
@@ -889,7 +969,7 @@ __global__ void __launch_bounds__(256) many_join_kernel(Kv4Attn a, Plan p) {
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t out_row = (int64_t)stripe * p.rows + srow;
+    const int64_t out_row = (int64_t)u.stripe * p.rows + srow;
     reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * kHD)[lane] =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     if (lane == 0 && a.lse) a.lse[out_row] = (top + log2f(sum)) * 0.6931471805599453f;
@@ -909,17 +989,16 @@ Shape shape_of(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq, bool lists) {
     return s;
 }
 
-// Splits of a unit's pages: the number that makes the waves of CTAs shortest,
-// in tiles; a wave costs about four tiles beside its own, a split's joining
-// about one more.
-int splits_of(int64_t units, int64_t tiles) {
+// CTAs a unit, at most: as many as the scratch holds; where the device does
+// not choose, the number of least cost for units of equal length.
+int splits_of(int64_t units, int64_t tiles, bool device_chooses) {
     int best = 1;
-    double least = 0.0;
+    float least = 0.0f;
     for (int s = 1; s <= kMaxSplits; ++s) {
         if (s > 1 && (units * s > kMaxParts || tiles < 2 * s)) break;
-        const double waves = (double)ceil_div(units * s, 148);
-        const double cost = waves * ((double)tiles / s + 4.0) + (s > 1 ? 3.0 + s : 0.0);
-        if (s == 1 || cost < least) best = s, least = cost;
+        const float cost = cost_of((float)(units * s), (float)ceil_div(tiles, s), 0.0f, s > 1,
+                                   true);
+        if (s == 1 || device_chooses || cost < least) best = s, least = cost;
     }
     return best;
 }
@@ -950,7 +1029,7 @@ int64_t kv4_attn_many_rows(const Kv4Shape &k) {
 
 int64_t kv4_attn_many_work_bytes(const Kv4Shape &k) {
     const Shape s = shape_of(k.n, k.Hq, k.Hkv, k.Lq, k.lists);
-    return SPARSTAR_KV4_WORK_ZEROS + part_bytes(s) +
+    return kHeadBytes + part_bytes(s) +
            (unpack_first(s, k) ? k.n * k.max_pages * k.Hkv * kPairBytes : 0);
 }
 
@@ -964,25 +1043,31 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
     p.rows = (int)s.rows;
     p.pairs = (int)s.pairs;
     p.nqb = (int)ceil_div(s.rows, kBlock);
-    p.splits = splits_of(s.units(), k.lists ? a.max_sel : c.max_pages);
-    p.sc = a.tau * 1.4426950408889634f;
-    p.halved = s.halved();
-    p.joins = p.halved || p.splits > 1;
-    p.parts = static_cast<float *>(a.work) + SPARSTAR_KV4_WORK_ZEROS / 4;
-    p.tiles = static_cast<uint8_t *>(a.work) + SPARSTAR_KV4_WORK_ZEROS + part_bytes(s);
-    p.tile_blocks = c.max_pages;
     const bool first = unpack_first(s, k);
+    const int64_t entries = k.lists ? a.max_sel : c.max_pages;  // of a unit, at most
+    p.halved = s.halved();
+    const bool chooses = first && !k.lists && !p.halved && (a.n > 1 || a.causal);
+    p.splits = splits_of(s.units(), p.halved ? ceil_div(entries, 2) : entries, chooses);
+    p.chunk = (int)ceil_div(entries > 0 ? entries : 1, p.splits);
+    p.chosen = chooses && p.splits > 1
+                   ? static_cast<int32_t *>(a.work) + SPARSTAR_KV4_WORK_ZEROS / 4
+                   : nullptr;
+    p.sc = a.tau * 1.4426950408889634f;
+    p.parts = static_cast<float *>(a.work) + kHeadBytes / 4;
+    p.tiles = static_cast<uint8_t *>(a.work) + kHeadBytes + part_bytes(s);
+    p.tile_blocks = c.max_pages;
     const auto kernel = first ? many_kernel<true> : many_kernel<false>;
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     if (first)
-        unpack_kernel<<<(unsigned)((int64_t)a.n * c.max_pages * c.Hkv), 256, 0, stream>>>(c, a, p);
+        unpack_kernel<<<(unsigned)((int64_t)a.n * c.max_pages * c.Hkv + (p.chosen ? 1 : 0)), 256,
+                        0, stream>>>(c, a, p);
     kernel<<<(unsigned)(s.units() * p.splits), first ? kThreads<true> : kThreads<false>,
              kSmemBytes, stream>>>(mq, c, a, p);
-    if (p.joins)
+    if (p.halved || p.splits > 1)
         many_join_kernel<<<(unsigned)(s.units() * (p.halved ? kBlock : kPartRows) / 8), 256, 0,
-                           stream>>>(a, p);
+                           stream>>>(c, a, p);
     return cudaGetLastError();
 }
 

@@ -428,9 +428,15 @@ def test_pages_behind_two_gibibytes(sp):
         q = queries(1, Hkv, Lq, D, BF16)
         want = sp.sparstar_kv4_attn(small, q)
         got = sp.sparstar_kv4_attn(cache, q, seqs=ints(1))
-        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
-    assert torch.equal(sp.sparstar_kv4_read(cache, 300, seqs=ints(1))[0],
-                       sp.sparstar_kv4_read(small, 300)[0])
+        # The tables' widths differ, so the pages may be split differently: each
+        # result has its weights (which sum to 1) rounded to bf16 by 2^-8 at
+        # most, and itself; |out| <= max |v|.  Sums and maxima are fp32.
+        size = float(v.abs().max()) * (1 + 2.0 ** -4)  # a value read is within half a step
+        assert float((got[0].float() - want[0].float()).abs().max()) <= 4 * size * 2.0 ** -8
+        assert float((got[1] - want[1]).abs().max()) <= 1e-4
+    for a, b in zip(sp.sparstar_kv4_read(cache, 300, seqs=ints(1)),
+                    sp.sparstar_kv4_read(small, 300)):
+        assert torch.equal(a, b)
 
 
 # ------------------------------------------------------------- together
