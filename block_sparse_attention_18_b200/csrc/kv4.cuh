@@ -89,6 +89,27 @@ __device__ __forceinline__ void kv4_transpose(uint32_t (&w)[8]) {
     for (int e = 0; e < 8; ++e) w[e] = r[kv4_nibble(e)];
 }
 
+// Bounded wait of one thread for a phase of an mbarrier; false after two
+// seconds.
+__device__ __forceinline__ bool kv4_wait(uint32_t bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        uint64_t t;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (t0 == 0) t0 = t;
+        if (t - t0 > 2000000000ull) return false;
+    }
+}
+
 __device__ __forceinline__ void kv4_flag(int32_t *status, int32_t bits) {
     if (status) atomicOr(status, bits);
 }

@@ -7,6 +7,8 @@
 // channel (the contraction of P V runs over tokens, and its operand pairs
 // tokens), so they pass through shared memory as words of eight channels and
 // are transposed eight tokens by eight channels in registers.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -16,74 +18,140 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The 32 values of one group as fp32.
-__device__ __forceinline__ void load_group(const __nv_bfloat16 *p, float (&x)[32]) {
+// Scale code of a group whose largest magnitude is a: a / 7 rounded to four
+// significant bits.  Two roundings decide as one would: the fp32 quotient can
+// only fall on a border M of five bits while a != 7 M if a - 7 M is less than
+// half of 2^-23 relative, and it is at least one unit of a's last place.
+__device__ __forceinline__ uint32_t scale_code(float a) {
+    const uint32_t bits = __float_as_uint(__fdiv_rn(a, 7.0f));
+    const int c = (int)((bits + 0x7ffffu + ((bits >> 20) & 1u)) >> 20) - (kScaleExp << 3);
+    return (uint32_t)(c < 0 ? 0 : (c > 255 ? 255 : c));
+}
+
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to integers, ties to even
+constexpr uint32_t kNibbles = 0x000f000fu;
+
+// Joins four pairs of codes (in the low nibbles of the halves) to a word.
+__device__ __forceinline__ uint32_t join_pairs(const uint32_t (&p)[4]) {
+    return (p[0] & kNibbles) | ((p[1] & kNibbles) << 4) | ((p[2] & kNibbles) << 8) |
+           ((p[3] & kNibbles) << 12);
+}
+
+// One group of 32 values in registers: bf16 pairs, or fp32.
+struct GroupBf16 {
+    uint32_t x[16];
+    __device__ void load(const __nv_bfloat16 *p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        for (int i = 0; i < 4; ++i) {
+            const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
         }
     }
-}
-__device__ __forceinline__ void load_group(const float *p, float (&x)[32]) {
+    // The largest magnitude; NaN when there is one.
+    __device__ float largest() const {
+        uint32_t m = x[0] & 0x7fff7fffu;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p) + i);
-        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+        for (int i = 1; i < 16; ++i)
+            asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x[i] & 0x7fff7fffu));
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;"
+            : "=f"(r)
+            : "f"(__uint_as_float(m << 16)), "f"(__uint_as_float(m & 0xffff0000u)));
+        return r;
     }
-}
+    __device__ float get(int i) const {
+        return __uint_as_float(i & 1 ? x[i / 2] & 0xffff0000u : x[i / 2] << 16);
+    }
+    __device__ void set(int i, float v) {  // v: a bf16 value
+        const uint32_t b = __float_as_uint(v);
+        x[i / 2] = i & 1 ? (x[i / 2] & 0xffffu) | (b & 0xffff0000u)
+                         : (x[i / 2] & 0xffff0000u) | (b >> 16);
+    }
+    // Codes of values 8 i .. 8 i + 7.  x / s is a tie or at least 2^-10 of a
+    // step away from one (eight and four significant bits), so the products
+    // with a reciprocal 2^-20 too large and one 2^-20 too small round alike
+    // except for a tie, where they round to its two neighbours: the larger
+    // one without its last bit is the even one.
+    __device__ uint32_t word(int i, float s) const {
+        const float r = __frcp_rn(s);
+        const float up = r * (1.0f + 0x1p-20f), down = r * (1.0f - 0x1p-20f);
+        uint32_t p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float a = get(8 * i + 2 * k), b = get(8 * i + 2 * k + 1);
+            const uint32_t u = __byte_perm(__float_as_uint(fmaf(a, up, kRound + 8.0f)),
+                                           __float_as_uint(fmaf(b, up, kRound + 8.0f)), 0x5410);
+            const uint32_t d = __byte_perm(__float_as_uint(fmaf(a, down, kRound + 8.0f)),
+                                           __float_as_uint(fmaf(b, down, kRound + 8.0f)), 0x5410);
+            p[k] = __vmaxu2(u, d) & ~((u ^ d) & 0x00010001u);
+        }
+        return join_pairs(p);
+    }
+};
+struct GroupF32 {
+    float x[32];
+    __device__ void load(const float *p) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 v = __ldcs(reinterpret_cast<const float4 *>(p) + i);
+            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+        }
+    }
+    __device__ float largest() const {
+        float m = fabsf(x[0]);
+#pragma unroll
+        for (int i = 1; i < 32; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x[i])));
+        return m;
+    }
+    __device__ float get(int i) const { return x[i]; }
+    __device__ void set(int i, float v) { x[i] = v; }
+    // n = rint(x * (1/s)) is off by one at most (the product is within 2^-22
+    // of the quotient), and x - n s is exact in an fma: its magnitude against
+    // s / 2 settles the nearest code, and n's last bit a tie.
+    __device__ uint32_t word(int i, float s) const {
+        const float r = __frcp_rn(s);
+        const uint32_t half = __float_as_uint(0.5f * s);
+        uint32_t p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t c[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float v = x[8 * i + 2 * k + h];
+                const float t = fmaf(v, r, kRound + 8.0f);
+                const uint32_t bits = __float_as_uint(t);
+                const uint32_t d = __float_as_uint(fmaf(-(t - (kRound + 8.0f)), s, v));
+                const bool step = (d & 0x7fffffffu) + (bits & 1u) > half;
+                c[h] = bits + (step ? ((int)d >> 31) | 1 : 0);
+            }
+            p[k] = __byte_perm(c[0], c[1], 0x5410);
+        }
+        return join_pairs(p);
+    }
+};
+template <typename T>
+using Group = typename std::conditional<std::is_same<T, float>::value, GroupF32, GroupBf16>::type;
 
 // Quantises one group: four words of codes and the scale code.  Returns
 // false when a value was beyond the range or NaN.
-//
-// Both decisions are exact.  The scale: a / 7 rounded to fp32 and then to
-// four bits can only differ from one rounding if the fp32 quotient falls on
-// a border M of five bits while a != 7 M; but then a - 7 M is at least one
-// unit of a's last place, 2^-23 relative, and the quotient is off by half of
-// 2^-23 at most.  The code: n = rint(x * (1/s)) is off by one at most (the
-// product is within 2^-22 of the quotient), and x - n s is exact in an fma,
-// so comparing it with s / 2 settles the nearest code and the ties.
-__device__ __forceinline__ bool quantise(float (&x)[32], uint32_t (&w)[4], uint32_t &code) {
-    bool fine = true;
-    float a = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        fine &= fabsf(x[i]) <= kKv4Limit;  // false for NaN
-        a = fmaxf(a, fabsf(x[i]));
-    }
+template <typename G>
+__device__ __forceinline__ bool quantise(G &x, uint32_t (&w)[4], uint32_t &code) {
+    float a = x.largest();
+    const bool fine = a <= kKv4Limit;  // false for NaN
     if (!fine) {
         a = 0.0f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -kKv4Limit), kKv4Limit) : 0.0f;
-            a = fmaxf(a, fabsf(x[i]));
+            const float v = x.get(i);
+            const float y = v == v ? fminf(fmaxf(v, -kKv4Limit), kKv4Limit) : 0.0f;
+            x.set(i, y);
+            a = fmaxf(a, fabsf(y));
         }
     }
-    const uint32_t bits = __float_as_uint(__fdiv_rn(a, 7.0f));
-    int c = (int)((bits + 0x7ffffu + ((bits >> 20) & 1u)) >> 20) - (kScaleExp << 3);
-    c = c < 0 ? 0 : (c > 255 ? 255 : c);
-    code = (uint32_t)c;
-    const float s = kv4_scale(code), r = __frcp_rn(s), half = 0.5f * s;
+    code = scale_code(a);
+    const float s = kv4_scale(code);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t word = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float v = x[8 * i + e];
-            float n = rintf(v * r);
-            const float d = fmaf(-n, s, v);  // exact
-            // One step toward v when n is not the nearest, or is odd in a tie.
-            const bool odd = ((int)n & 1) != 0;
-            if (fabsf(d) > half || (fabsf(d) == half && odd)) n += copysignf(1.0f, d);
-            n = fminf(fmaxf(n, -7.0f), 7.0f);
-            word |= (uint32_t)((int)n + 8) << (4 * kv4_nibble(e));
-        }
-        w[i] = word;
-    }
+    for (int i = 0; i < 4; ++i) w[i] = x.word(i, s);
     return fine;
 }
 
@@ -160,9 +228,9 @@ __global__ void __launch_bounds__(kThreads)
         const bool is_v = it >= items;
         const int u = is_v ? it - items : it;
         const int slot = first + u / G, g = u % G;
-        float x[32];
+        Group<T> x;
         uint32_t w[4], code;
-        load_group((is_v ? v : k) + (row + slot + sp.shift) * D + g * kGroup, x);
+        x.load((is_v ? v : k) + (row + slot + sp.shift) * D + g * kGroup);
         fine &= quantise(x, w, code);
         if (is_v) {
 #pragma unroll

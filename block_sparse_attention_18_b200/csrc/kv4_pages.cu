@@ -3,10 +3,14 @@
 // per page, tables and lengths per sequence; a page is free when its count is
 // 0, so the state has one form and every call's result depends on it alone.
 //
-// A planning kernel (one CTA) decides and writes the tables; pages that have
-// to be copied go on a list that a second kernel, over the whole GPU, works
-// off.  The plan is bound by latency (a chain of a few dependent loads, and
-// one pass over the counts when pages are taken), the copies by HBM traffic.
+// One CTA decides and writes the tables; pages that have to be copied go on
+// a list that a second kernel, over the whole GPU, works off: plain loads and
+// stores for the few pages of a resize (at most one a sequence), bulk copies
+// through shared memory for the many of a deep copy or a compaction.  The
+// second kernel is set up while the first runs.  The plan is bound by latency
+// (a chain of a few dependent loads, and one pass over the counts when pages
+// are taken), the copies by HBM traffic.  A cluster of eight that plans and
+// copies in one launch was slower (two resizes and a fork: 19.5 us against 15.9).
 #include <cuda_runtime.h>
 
 #include "kv4.cuh"
@@ -17,13 +21,24 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kWarps = kPlanThreads / 32;
 
-// Scratch (int32): a head, three lists of n_pages, three of n_seqs.
+// An entry of a resize or deep fork.
+struct Entry {
+    int32_t slot, from;  // slot changed, slot copied (-1: none)
+    int32_t begin;       // first page taken; kNothing, kRefused
+    int32_t rank;        // of it among the pages that the call takes
+    int32_t old_len, new_len;
+};
+constexpr int kNothing = -1, kRefused = -2;
+
+// Scratch (int32): a head, three lists of n_pages, n_seqs entries and owners.
 struct Work {
     int32_t *pairs;  // [0] pages to copy, [1] live pages (compact)
     int32_t *to, *from, *moved;
-    int32_t *owner, *begin, *rank;
+    int32_t *owner;
+    Entry *entries;
 };
 constexpr int kHead = 16;
+constexpr int kInside = 512;  // entries that fit shared memory
 __host__ __device__ inline Work work_of(const Kv4 &c) {
     Work w;
     w.pairs = c.work;
@@ -31,8 +46,7 @@ __host__ __device__ inline Work work_of(const Kv4 &c) {
     w.from = w.to + c.n_pages;
     w.moved = w.from + c.n_pages;
     w.owner = w.moved + c.n_pages;
-    w.begin = w.owner + c.n_seqs;
-    w.rank = w.begin + c.n_seqs;
+    w.entries = reinterpret_cast<Entry *>(w.owner + c.n_seqs);
     return w;
 }
 
@@ -92,95 +106,127 @@ __device__ int find_free(const Kv4 &c, int want, int32_t *list, int32_t *sums) {
     return found < want ? found : want;
 }
 
-// True when no earlier entry names the slot (owner[slot] = the lowest one).
-__device__ void mark_owners(const Kv4 &c, const Work &w, const int32_t *slots, int n) {
-    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-        const int s = kv4_slot(c, slots, i);
-        if (s >= 0) w.owner[s] = 0x7fffffff;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-        const int s = kv4_slot(c, slots, i);
-        if (s >= 0) atomicMin(w.owner + s, i);
-    }
-    __syncthreads();
-}
-
-// What entry i of a resize (src NULL) or deep fork asks for.
-struct Ask {
-    int slot, from_slot, old_len, new_len;
-    bool ok;
-};
-__device__ Ask ask_of(const Kv4 &c, const Work &w, const int32_t *slots, const int32_t *src,
-                      const int32_t *lens, int i) {
-    Ask a;
-    a.slot = kv4_slot(c, slots, i);
-    a.from_slot = -1;
-    a.old_len = a.new_len = 0;
-    a.ok = a.slot >= 0 && (!slots || __ldcg(w.owner + a.slot) == i);
-    if (!a.ok) return a;
-    a.old_len = kv4_len(c, a.slot);
-    if (src) {
-        a.from_slot = kv4_slot(c, src, i);
-        a.ok = a.from_slot >= 0 && a.old_len == 0;
-        const int have = a.ok ? kv4_len(c, a.from_slot) : 0;
-        a.new_len = lens ? __ldg(lens + i) : have;
-        a.ok = a.ok && a.new_len >= 0 && a.new_len <= have;
-    } else {
-        a.new_len = __ldg(lens + i);
-        a.ok = a.new_len >= 0 && a.new_len <= (int64_t)c.max_pages * kBlock;
-    }
-    return a;
-}
-
 __device__ __forceinline__ int pages_of(int len) { return (len + kBlock - 1) / kBlock; }
 __device__ __forceinline__ bool is_page(const Kv4 &c, int p) { return p >= 0 && p < c.n_pages; }
 
-// A fork entry whose source is one of the call's destinations is left out
-// (fork_shared_kernel, whose CTAs run at the same time, needs that rule).
-__device__ bool is_dst(const int32_t *dst, int n, int slot) {
-    for (int i = 0; i < n; ++i)
-        if (__ldg(dst + i) == slot) return true;
-    return false;
+// Copies the listed pages, a page of one head (17 or 9 KB) at a time: a warp
+// has one stage of shared memory, brings the piece in with one bulk copy and
+// sends it off with another.  The CTA's 12 or 24 stages (209 KB) are in flight
+// at once, which a few hundred registers could not hold.
+constexpr int kStageBytes = 12 * kv4_page_bytes(128);
+constexpr int kMaxStages = kStageBytes / kv4_page_bytes(64);
+__device__ void copy_pages(const Kv4 &c, const Work &w, int pairs, int cta, int ctas,
+                           uint64_t *bars, uint8_t *smem, int32_t *status) {
+    const int bytes = kv4_page_bytes(c.D), stages = kStageBytes / bytes;
+    const int warp = threadIdx.x >> 5;
+    if (warp >= stages || (threadIdx.x & 31) != 0) return;
+    uint64_t *mbar = bars + warp;
+    const uint32_t bar = (uint32_t)__cvta_generic_to_shared(mbar);
+    const uint32_t stage = (uint32_t)__cvta_generic_to_shared(smem + warp * bytes);
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    uint32_t phase = 0;
+    const int64_t all = (int64_t)pairs * c.Hkv;
+    for (int64_t it = (int64_t)cta * stages + warp; it < all; it += (int64_t)ctas * stages) {
+        const int k = (int)(it / c.Hkv), h = (int)(it - (int64_t)k * c.Hkv);
+        const int from = __ldcg(w.from + k), to = __ldcg(w.to + k);
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                     "r"(bytes)
+                     : "memory");
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+            "[%3];" ::"r"(stage),
+            "l"(c.pages + ((int64_t)from * c.Hkv + h) * bytes), "r"(bytes), "r"(bar)
+            : "memory");
+        if (!kv4_wait(bar, phase)) {
+            kv4_flag(status, SPARSTAR_STATUS_TIMEOUT);
+            break;
+        }
+        phase ^= 1u;
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                         c.pages + ((int64_t)to * c.Hkv + h) * bytes),
+                     "r"(stage), "r"(bytes)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // resize (src NULL: slots, lens) and deep fork (src, slots = dst, lens).
-__global__ void __launch_bounds__(kPlanThreads)
-    plan_kernel(Kv4 c, const int32_t *slots, const int32_t *src, const int32_t *lens, int n,
-                int32_t *status) {
+__device__ void plan(const Kv4 &c, const int32_t *slots, const int32_t *src, const int32_t *lens,
+                     int n, int32_t *status) {
     __shared__ int64_t needs[kWarps];
     __shared__ int32_t sums[kWarps], n_pairs;
+    __shared__ Entry inside[kInside];
     const Work w = work_of(c);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Entry *entries = n <= kInside ? inside : w.entries;
     if (threadIdx.x == 0) n_pairs = 0;
-    if (slots) mark_owners(c, w, slots, n);
-    // Pass 1: what each entry needs (negative begin: nothing to take), its
-    // first rank among the pages taken.  Reads the counts before any change.
+    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+        entries[i].slot = kv4_slot(c, slots, i);
+        entries[i].from = src ? kv4_slot(c, src, i) : -1;
+    }
+    __syncthreads();
+    // A slot belongs to the lowest entry that names it: few entries compare
+    // with the ones before, many mark their slots.
+    const bool marks = slots && n > kInside;
+    if (marks) {
+        for (int i = threadIdx.x; i < n; i += kPlanThreads)
+            if (entries[i].slot >= 0) w.owner[entries[i].slot] = 0x7fffffff;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += kPlanThreads)
+            if (entries[i].slot >= 0) atomicMin(w.owner + entries[i].slot, i);
+        __syncthreads();
+    }
+    // Pass 1: what each entry needs and its first rank among the pages taken.
+    // Reads the counts before any change.
     int64_t wanted = 0;
     for (int base = 0; base < n; base += kPlanThreads) {
         const int i = base + threadIdx.x;
         int64_t need = 0;
-        int begin = -1;
+        Entry e{-1, -1, kRefused, 0, 0, 0};
         if (i < n) {
-            Ask a = ask_of(c, w, slots, src, lens, i);
-            if (a.ok && src && is_dst(slots, n, a.from_slot)) a.ok = false;
-            if (!a.ok) {
-                kv4_flag(status, SPARSTAR_STATUS_BAD_INDEX);
-                begin = -2;
-            } else if (a.new_len > a.old_len) {
-                begin = pages_of(a.old_len);
-                if (a.old_len % kBlock) {
-                    const int tail = c.table[(int64_t)a.slot * c.max_pages + begin - 1];
-                    if (is_page(c, tail) && c.refs[tail] > 1) --begin;
+            e.slot = entries[i].slot, e.from = entries[i].from;
+            bool ok = e.slot >= 0;
+            if (ok && marks) ok = __ldcg(w.owner + e.slot) == i;
+            else if (ok && slots)
+                for (int k = 0; k < i; ++k) ok &= entries[k].slot != e.slot;
+            if (ok) {
+                e.old_len = kv4_len(c, e.slot);
+                if (src) {
+                    // An entry whose source is a destination of the call is
+                    // left out (fork_shared_kernel's CTAs need that rule).
+                    ok = e.from >= 0 && e.old_len == 0;
+                    for (int k = 0; k < n && ok; ++k) ok = entries[k].slot != e.from;
+                    const int have = ok ? kv4_len(c, e.from) : 0;
+                    e.new_len = lens ? __ldg(lens + i) : have;
+                    ok = ok && e.new_len >= 0 && e.new_len <= have;
+                } else {
+                    e.new_len = __ldg(lens + i);
+                    ok = e.new_len >= 0 && e.new_len <= (int64_t)c.max_pages * kBlock;
                 }
-                need = pages_of(a.new_len) - begin;
+            }
+            if (!ok) {
+                kv4_flag(status, SPARSTAR_STATUS_BAD_INDEX);
+            } else if (e.new_len > e.old_len) {
+                e.begin = pages_of(e.old_len);
+                if (e.old_len % kBlock) {
+                    const int tail = c.table[(int64_t)e.slot * c.max_pages + e.begin - 1];
+                    if (is_page(c, tail) && c.refs[tail] > 1) --e.begin;
+                }
+                need = pages_of(e.new_len) - e.begin;
+            } else {
+                e.begin = kNothing;
             }
         }
         int64_t total;
         const int64_t rank = wanted + block_scan(need, needs, total);
+        e.rank = rank <= c.n_pages ? (int)rank : c.n_pages + 1;
+        // Slots and sources stay: other entries compare with them.
         if (i < n) {
-            w.begin[i] = begin;
-            w.rank[i] = rank <= c.n_pages ? (int)rank : c.n_pages + 1;
+            entries[i].begin = e.begin, entries[i].rank = e.rank;
+            entries[i].old_len = e.old_len, entries[i].new_len = e.new_len;
         }
         wanted += total;
     }
@@ -188,49 +234,74 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int limit = wanted < c.n_pages ? (int)wanted : c.n_pages;
     const int found = limit > 0 ? find_free(c, limit, w.moved, sums) : 0;
     __syncthreads();
-    // Pass 2: one warp an entry.
-    for (int i = warp; i < n; i += kWarps) {
-        const int begin = __ldcg(w.begin + i), rank = __ldcg(w.rank + i);
-        if (begin == -2) continue;
-        const Ask a = ask_of(c, w, slots, src, lens, i);
-        int32_t *row = c.table + (int64_t)a.slot * c.max_pages;
-        const int had = pages_of(a.old_len), have = pages_of(a.new_len);
-        if (begin >= 0) {
-            const int need = have - begin;
-            if (need > 0 && (rank > found || need > found - rank)) {
-                if (lane == 0) kv4_flag(status, SPARSTAR_STATUS_NO_PAGES);
-                continue;
+    // Pass 2: tables and counts; a few warps an entry, four pages a lane at once.
+    const int per = n >= kWarps ? 1 : kWarps / n;  // warps an entry
+    for (int i = warp / per; i < n && warp < per * n; i += kWarps / per) {
+        const Entry e = entries[i];
+        if (e.begin == kRefused) continue;
+        int32_t *row = c.table + (int64_t)e.slot * c.max_pages;
+        const int had = pages_of(e.old_len), have = pages_of(e.new_len);
+        const bool takes = e.begin >= 0;
+        const int first = takes ? e.begin : have, last = takes ? have : had;
+        if (takes && last > first && (e.rank > found || last - first > found - e.rank)) {
+            if (lane == 0) kv4_flag(status, SPARSTAR_STATUS_NO_PAGES);
+            continue;
+        }
+        const int32_t *from = src ? c.table + (int64_t)e.from * c.max_pages : nullptr;
+        for (int j0 = first + (warp % per) * 128 + lane; j0 < last; j0 += per * 128) {
+            int fresh[4], old[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = j0 + 32 * k;
+                fresh[k] = old[k] = -1;
+                if (j >= last) continue;
+                if (takes) fresh[k] = __ldcg(w.moved + e.rank + j - first);
+                // What a page taken is a copy of (a source's page, the shared
+                // partial page), or the page given up.
+                if (!takes || from || j < had) old[k] = __ldcg((from ? from : row) + j);
             }
-            const int32_t *from =
-                src ? c.table + (int64_t)a.from_slot * c.max_pages : nullptr;
-            for (int j = lane; j < need; j += 32) {
-                const int page = __ldcg(w.moved + rank + j);
-                int copy_of = -1;
-                if (from) {
-                    copy_of = from[begin + j];
-                } else if (begin + j < had) {  // the shared partial page
-                    copy_of = row[begin + j];
-                    if (is_page(c, copy_of)) atomicSub(c.refs + copy_of, 1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = j0 + 32 * k;
+                if (j >= last) continue;
+                const bool real = is_page(c, old[k]);
+                if (real && !from) atomicSub(c.refs + old[k], 1);
+                row[j] = fresh[k];
+                if (!takes) continue;
+                c.refs[fresh[k]] = 1;
+                if (real) {
+                    const int at = atomicAdd(&n_pairs, 1);
+                    w.to[at] = fresh[k];
+                    w.from[at] = old[k];
                 }
-                row[begin + j] = page;
-                c.refs[page] = 1;
-                if (is_page(c, copy_of)) {
-                    const int p = atomicAdd(&n_pairs, 1);
-                    w.to[p] = page;
-                    w.from[p] = copy_of;
-                }
-            }
-        } else {
-            for (int j = have + lane; j < had; j += 32) {
-                const int page = row[j];
-                if (is_page(c, page)) atomicSub(c.refs + page, 1);
-                row[j] = -1;
             }
         }
-        if (lane == 0) c.lens[a.slot] = a.new_len;
+        if (lane == 0 && warp % per == 0) c.lens[e.slot] = e.new_len;
     }
     __syncthreads();
     if (threadIdx.x == 0) w.pairs[0] = n_pairs;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    plan_kernel(Kv4 c, const int32_t *slots, const int32_t *src, const int32_t *lens, int n,
+                int32_t *status) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    plan(c, slots, src, lens, n, status);
+}
+
+// Copies a short list: 16 bytes a thread.
+__global__ void __launch_bounds__(256) copy_few_kernel(Kv4 c) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Work w = work_of(c);
+    const int pairs = w.pairs[0];
+    const int vecs = c.Hkv * (kv4_page_bytes(c.D) / 16);  // of a page
+    const int chunks = (vecs + 255) / 256;
+    for (int64_t it = blockIdx.x; it < (int64_t)chunks * pairs; it += gridDim.x) {
+        const int k = (int)(it / chunks), at = (int)(it - (int64_t)k * chunks) * 256 + threadIdx.x;
+        if (at < vecs)
+            reinterpret_cast<uint4 *>(c.pages)[(int64_t)w.to[k] * vecs + at] =
+                reinterpret_cast<const uint4 *>(c.pages)[(int64_t)w.from[k] * vecs + at];
+    }
 }
 
 // Shared fork: one CTA an entry.  No entry reads what another writes: a
@@ -270,6 +341,7 @@ __global__ void __launch_bounds__(256)
 
 // Which pages move where, the counts after it.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Kv4 c, int32_t *n_live) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int32_t sums[kWarps];
     const Work w = work_of(c);
     int live = 0, total;
@@ -305,18 +377,16 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Kv4 c, int32
 
 // Copies the listed pages; with `remap`, also renames the moved ones in the
 // tables.
-__global__ void __launch_bounds__(256) copy_kernel(Kv4 c, bool remap) {
+constexpr int kCopyThreads = 32 * kMaxStages;
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_kernel(Kv4 c, bool remap, int32_t *status) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t bars[kMaxStages];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Work w = work_of(c);
     const int pairs = w.pairs[0];
     if (pairs == 0) return;
-    const int64_t bytes = (int64_t)c.Hkv * kv4_page_bytes(c.D), vecs = bytes / 16;
-    const int64_t all = vecs * pairs;
-    for (int64_t v = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; v < all;
-         v += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t k = v / vecs, at = v % vecs;
-        reinterpret_cast<uint4 *>(c.pages + w.to[k] * bytes)[at] =
-            reinterpret_cast<const uint4 *>(c.pages + w.from[k] * bytes)[at];
-    }
+    copy_pages(c, w, pairs, blockIdx.x, gridDim.x, bars, smem, status);
     if (!remap) return;
     const int live = w.pairs[1];
     const int64_t entries = (int64_t)c.n_seqs * c.max_pages;
@@ -329,19 +399,42 @@ __global__ void __launch_bounds__(256) copy_kernel(Kv4 c, bool remap) {
     }
 }
 
-constexpr int kCopyCtas = 148 * 8;
+// A kernel that the plan's lets start early; it waits for the plan's end.
+template <typename... Args>
+cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned block, size_t smem,
+                         cudaStream_t stream, Args... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+cudaError_t launch_copy(const Kv4 &c, bool remap, int32_t *status, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(
+        copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes);
+    if (e != cudaSuccess) return e;
+    return launch_after(copy_kernel, 148, kCopyThreads, kStageBytes, stream, c, remap, status);
+}
 
 }  // namespace
 
 int64_t kv4_work_ints(int64_t n_pages, int64_t n_seqs) {
-    return kHead + 3 * n_pages + 3 * n_seqs;
+    return kHead + 3 * n_pages + 7 * n_seqs;
 }
 
 cudaError_t launch_kv4_resize(const Kv4 &c, const int32_t *seqs, const int32_t *new_lens, int n,
                               int32_t *status, cudaStream_t stream) {
     plan_kernel<<<1, kPlanThreads, 0, stream>>>(c, seqs, nullptr, new_lens, n, status);
-    copy_kernel<<<kCopyCtas, 256, 0, stream>>>(c, false);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_after(copy_few_kernel, 148 * 4, 256, 0, stream, c);
 }
 
 cudaError_t launch_kv4_fork(const Kv4 &c, const int32_t *src, const int32_t *dst,
@@ -349,7 +442,9 @@ cudaError_t launch_kv4_fork(const Kv4 &c, const int32_t *src, const int32_t *dst
                             cudaStream_t stream) {
     if (deep) {
         plan_kernel<<<1, kPlanThreads, 0, stream>>>(c, dst, src, len, n, status);
-        copy_kernel<<<kCopyCtas, 256, 0, stream>>>(c, false);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        return launch_copy(c, false, status, stream);
     } else {
         fork_shared_kernel<<<n, 256, 0, stream>>>(c, src, dst, len, n, status);
     }
@@ -358,8 +453,9 @@ cudaError_t launch_kv4_fork(const Kv4 &c, const int32_t *src, const int32_t *dst
 
 cudaError_t launch_kv4_compact(const Kv4 &c, int32_t *n_live, cudaStream_t stream) {
     compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(c, n_live);
-    copy_kernel<<<kCopyCtas, 256, 0, stream>>>(c, true);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_copy(c, true, nullptr, stream);
 }
 
 }  // namespace sparstar
