@@ -278,7 +278,7 @@ def check_attn(sp, cache, q, expect=0, **kw):
     bf16); sums over all tokens add 4 e a page and 2 e a token of one.
     The output rounds once more.
     """
-    D, pages = cache.D, max(1, int(cache.max_pages))
+    D, pages = cache.D, max(1, -(-int(cache.lens.max()) // BLOCK))
     status = new_status()
     ref = model(cache)
     args = {k: (None if v is None else v.cpu().numpy() if torch.is_tensor(v) else v)
@@ -319,8 +319,9 @@ def queries(n, Hq, Lq, D, dtype, seed=0, scale=1.0):
     ([2100, 9], 16, 1, 2),                # 32 rows
 ])
 @pytest.mark.parametrize("causal", [False, True])
-def test_attention_of_few_rows(sp, D, dtype, lens, Hq, Hkv, Lq, causal):
-    cache = filled(sp, lens, Hkv, D, seed=sum(lens))
+@pytest.mark.parametrize("width", [None, 1300])  # wide tables: the split for long caches
+def test_attention_of_few_rows(sp, D, dtype, lens, Hq, Hkv, Lq, causal, width):
+    cache = filled(sp, lens, Hkv, D, seed=sum(lens), max_pages=width)
     check_attn(sp, cache, queries(len(lens), Hq, Lq, D, dtype), causal=causal)
 
 
@@ -399,6 +400,14 @@ def test_what_lies_behind_a_sequence_does_not_matter(sp, Lq):
     vals.view(128, 64)[:, 36:] = 0
     b = check_attn(sp, cache, q)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (64, BF16), (128, F32)])
+def test_attention_of_a_long_ragged_batch(sp, D, dtype):
+    # Units that begin and end inside a warp's part, and ones over many CTAs.
+    lens = [9000, 1, 130, 260, 4000, 0, 90, 129, 1000, 640, 17000, 300]
+    cache = filled(sp, lens, 2, D, seed=5)
+    check_attn(sp, cache, queries(len(lens), 4, 1, D, dtype))
 
 
 @pytest.mark.parametrize("Lq", [1, 300])
