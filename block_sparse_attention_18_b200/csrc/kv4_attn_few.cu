@@ -393,12 +393,12 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         if (a.lse)
             for (int64_t k = threadIdx.x; k < rows; k += kThreads) a.lse[i * rows + k] = -INFINITY;
     }
-    // This part: an equal piece of the CTA's, the last ones shorter or
-    // empty.
+    // This part: an equal piece of the CTA's tiles, the first ones a tile
+    // longer; parts with tiles are neighbours.
     const int64_t c0 = min(share * blockIdx.x, total), c1 = min(c0 + share, total);
-    const int64_t piece = ((uint32_t)(c1 - c0) + kParts - 1) / kParts;
-    const int64_t start = min(c0 + piece * part, c1);
-    const int x1 = (int)(min(start + piece, c1) - start);  // tiles of the part
+    const uint32_t piece = (uint32_t)(c1 - c0) / kParts, rest = (uint32_t)(c1 - c0) % kParts;
+    const int64_t start = c0 + (int64_t)piece * part + min((uint32_t)part, rest);
+    const int x1 = (int)(piece + ((uint32_t)part < rest ? 1 : 0));  // tiles of the part
     int x = 0;
     const int slot_id = blockIdx.x * kParts + part;
     uint8_t *ring = smem + part * kStages * kHalf;
