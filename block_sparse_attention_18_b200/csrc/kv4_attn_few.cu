@@ -361,7 +361,11 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     // Partial results of the parts, in the order of the line: the end of a
     // unit inside part k (2 k), what the part's end leaves (2 k + 1).
     __shared__ int32_t entry[2 * kParts], edges[2 * kParts];
-    __shared__ int32_t cross[2], span[2][2], n_cross;
+    // Units with partial results: which entries, first row, rows; flags as edges.
+    __shared__ int32_t group_uid[2 * kParts], group_flags[2 * kParts], group_rows[2 * kParts];
+    __shared__ uint32_t group_entries[2 * kParts];
+    __shared__ int64_t group_row[2 * kParts];
+    __shared__ int32_t cross[2], span[2][2], n_cross, n_groups;
     const int part = (threadIdx.x >> 5) / kPair, member = (threadIdx.x >> 5) % kPair;
     const int lane = threadIdx.x & 31;
     const int r = lane >> 2, j = lane & 3;
@@ -883,49 +887,58 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
             sl[w * R + lane] = rec[R * D + R + lane];
         }
     }
-    if (threadIdx.x == 0) n_cross = 0;
-    __syncthreads();
-    for (int e0 = 0; e0 < 2 * kParts;) {
-        const int id = entry[e0];
-        if (id < 0) {
-            ++e0;
-            continue;
-        }
-        int e1 = e0 + 1, last = e0;  // entries e0 .. last are this unit's, or empty
-        uint32_t mine = 1u << e0;
-        for (; e1 < 2 * kParts && (entry[e1] == id || entry[e1] < 0); ++e1)
-            if (entry[e1] == id) last = e1, mine |= 1u << e1;
-        const bool begins = (edges[e0] & 1) != 0, whole = begins && (edges[last] & 2);
-        const Unit g = unit_of<R>(c, a, p, id);
-        float *rec = p.joins + (int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * kRecord;
-        for (int v = threadIdx.x; v < R * D / 4; v += kThreads) {
-            const int row = v / (D / 4), d = v % (D / 4) * 4;
-            Part4 sum;
-            float top = -INFINITY;
-            auto each = [&](auto f) {
-                for (uint32_t left = mine; left; left &= left - 1) {
-                    const int en = __ffs(left) - 1;
-#pragma unroll
-                    for (int w = 0; w < kPair; ++w)
-                        f((en & 1 ? 0 : kWarps) + (en >> 1) * kPair + w);
-                }
-            };
-            each([&](int w) { top = fmaxf(top, sm[w * R + row]); });
-            sum.top = top;
-            each([&](int w) {
-                sum.add(sm[w * R + row], sl[w * R + row],
-                        *reinterpret_cast<const float4 *>(so + (w * R + row) * kRow + d));
-            });
-            if (!whole) {
-                *reinterpret_cast<float4 *>(rec + 4 * v) = sum.acc;
-                if (d == 0) rec[R * D + row] = sum.top, rec[R * D + R + row] = sum.sum;
-            } else if (row < g.rows) {
-                sum.write(static_cast<T *>(a.out) + (g.row + row) * D + d,
-                          d == 0 && a.lse ? a.lse + g.row + row : nullptr);
+    if (threadIdx.x == 0) {
+        // Entries of one unit lie side by side, empty ones between them.
+        int n = 0, id = -1;
+        for (int en = 0; en < 2 * kParts; ++en) {
+            if (entry[en] < 0) continue;
+            if (entry[en] != id) {
+                id = group_uid[n] = entry[en];
+                group_entries[n] = 0;
+                group_flags[n++] = edges[en] & 1;
             }
+            group_entries[n - 1] |= 1u << en;
+            group_flags[n - 1] |= edges[en] & 2;
         }
-        if (!whole && threadIdx.x == 0) cross[n_cross++] = id;
-        e0 = last + 1;
+        n_groups = n;
+        n_cross = 0;
+    }
+    __syncthreads();
+    for (int g = threadIdx.x; g < n_groups; g += kThreads) {
+        const Unit un = unit_of<R>(c, a, p, group_uid[g]);
+        group_row[g] = un.row;
+        group_rows[g] = un.rows;
+        // At most two go on in other CTAs: the first and the last.
+        if (group_flags[g] != 3) cross[atomicAdd(&n_cross, 1)] = group_uid[g];
+    }
+    __syncthreads();
+    for (int it = threadIdx.x; it < n_groups * (R * D / 4); it += kThreads) {
+        const int g = it / (R * D / 4), v = it % (R * D / 4);
+        const int row = v / (D / 4), d = v % (D / 4) * 4;
+        Part4 sum;
+        float top = -INFINITY;
+        auto each = [&](auto f) {
+            for (uint32_t left = group_entries[g]; left; left &= left - 1) {
+                const int en = __ffs(left) - 1;
+#pragma unroll
+                for (int w = 0; w < kPair; ++w) f((en & 1 ? 0 : kWarps) + (en >> 1) * kPair + w);
+            }
+        };
+        each([&](int w) { top = fmaxf(top, sm[w * R + row]); });
+        sum.top = top;
+        each([&](int w) {
+            sum.add(sm[w * R + row], sl[w * R + row],
+                    *reinterpret_cast<const float4 *>(so + (w * R + row) * kRow + d));
+        });
+        if (group_flags[g] != 3) {
+            float *rec = p.joins + (int64_t)(blockIdx.x * 2 + (group_flags[g] & 1)) * kRecord;
+            *reinterpret_cast<float4 *>(rec + 4 * v) = sum.acc;
+            if (d == 0) rec[R * D + row] = sum.top, rec[R * D + R + row] = sum.sum;
+        } else if (row < group_rows[g]) {
+            const int64_t out_row = group_row[g] + row;
+            sum.write(static_cast<T *>(a.out) + out_row * D + d,
+                      d == 0 && a.lse ? a.lse + out_row : nullptr);
+        }
     }
     // ---------------- units of several CTAs: the last one to arrive joins them
     __syncthreads();
