@@ -462,6 +462,7 @@ class Kv4Cache:
         self.Hkv, self.D, self.device = pages.shape[1], D, pages.device
         self.index = pages.get_device()
         self._work_of = {}  # stream handle -> scratch of its attention calls
+        self._need = {}     # sizes of an attention call -> bytes of its scratch
         self._struct = _Kv4Struct(pages.data_ptr(), refs.data_ptr(), table.data_ptr(),
                                   lens.data_ptr(), work.data_ptr(), n_pages, n_seqs,
                                   table.shape[1], pages.shape[1], D)
@@ -514,82 +515,88 @@ def _kv4_status(cache, status):
     return None if status is None else _kv4_tensor(cache, status, "status", torch.int32, (1,))
 
 
-class _Kv4Call:
-    """Context of a call: the cache's device is the current one, and so is the
-    stream given; yields the stream's handle."""
+def _kv4_elsewhere(cache, stream):
+    """Whether a call has to switch to the cache's device or another stream."""
+    return stream is not None or torch._C._cuda_getDevice() != cache.index
 
-    __slots__ = ("device", "stream", "index")
+
+class _Kv4There:
+    """The cache's device and the stream given as the current ones."""
 
     def __init__(self, cache, stream):
-        self.index = cache.index
-        self.device = torch.cuda.device(cache.index) \
-            if torch._C._cuda_getDevice() != cache.index else None
-        self.stream = None if stream is None else torch.cuda.stream(stream)
+        self.device, self.stream = torch.cuda.device(cache.index), torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.device is not None:
-            self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
+        self.device.__enter__()
+        self.stream.__enter__()
 
     def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        if self.device is not None:
-            self.device.__exit__(*exc)
+        self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
         return False
+
+
+def _kv4_raw_stream(cache):
+    return torch._C._cuda_getCurrentRawStream(cache.index)
 
 
 def sparstar_kv4_resize(cache: Kv4Cache, new_lens, seqs=None, status=None, stream=None):
     """Sets the lengths of n sequences (0 frees one); takes and gives pages."""
+    if _kv4_elsewhere(cache, stream):
+        with _Kv4There(cache, stream):
+            return sparstar_kv4_resize(cache, new_lens, seqs, status)
     n = new_lens.numel()
-    with _Kv4Call(cache, stream) as s:
-        _check(lib.sparstar_kv4_resize(cache._struct, _kv4_ints(cache, seqs, "seqs", n),
-                                       _kv4_ints(cache, new_lens, "new_lens", n), n,
-                                       _kv4_status(cache, status), s),
-               "sparstar_kv4_resize")
+    _check(lib.sparstar_kv4_resize(cache._struct, _kv4_ints(cache, seqs, "seqs", n),
+                                   _kv4_ints(cache, new_lens, "new_lens", n), n,
+                                   _kv4_status(cache, status), _kv4_raw_stream(cache)),
+           "sparstar_kv4_resize")
 
 
 def sparstar_kv4_fork(cache: Kv4Cache, src, dst, lens=None, deep: bool = False, status=None,
                       stream=None):
     """Empty sequences dst take the tokens of src: shared pages, or (deep) copies."""
+    if _kv4_elsewhere(cache, stream):
+        with _Kv4There(cache, stream):
+            return sparstar_kv4_fork(cache, src, dst, lens, deep, status)
     n = src.numel()
-    with _Kv4Call(cache, stream) as s:
-        _check(lib.sparstar_kv4_fork(cache._struct, _kv4_ints(cache, src, "src", n),
-                                     _kv4_ints(cache, dst, "dst", n),
-                                     _kv4_ints(cache, lens, "lens", n), n, int(bool(deep)),
-                                     _kv4_status(cache, status), s),
-               "sparstar_kv4_fork")
+    _check(lib.sparstar_kv4_fork(cache._struct, _kv4_ints(cache, src, "src", n),
+                                 _kv4_ints(cache, dst, "dst", n),
+                                 _kv4_ints(cache, lens, "lens", n), n, int(bool(deep)),
+                                 _kv4_status(cache, status), _kv4_raw_stream(cache)),
+           "sparstar_kv4_fork")
 
 
 def sparstar_kv4_compact(cache: Kv4Cache, n_live=None, stream=None):
     """Moves the live pages to the lowest places; returns their number (device)."""
-    with _Kv4Call(cache, stream) as s:
-        if n_live is None:
-            n_live = torch.empty(1, dtype=torch.int32, device=cache.device)
-        _check(lib.sparstar_kv4_compact(cache._struct,
-                                        _kv4_tensor(cache, n_live, "n_live", torch.int32, (1,)),
-                                        s), "sparstar_kv4_compact")
+    if _kv4_elsewhere(cache, stream):
+        with _Kv4There(cache, stream):
+            return sparstar_kv4_compact(cache, n_live)
+    if n_live is None:
+        n_live = torch.empty(1, dtype=torch.int32, device=cache.device)
+    _check(lib.sparstar_kv4_compact(cache._struct,
+                                    _kv4_tensor(cache, n_live, "n_live", torch.int32, (1,)),
+                                    _kv4_raw_stream(cache)), "sparstar_kv4_compact")
     return n_live
 
 
 def sparstar_kv4_write(cache: Kv4Cache, k, v, seqs=None, starts=None, counts=None, status=None,
                        stream=None):
     """Stores k, v [n, Hkv, T, D] at positions starts (default: the last T)."""
+    if _kv4_elsewhere(cache, stream):
+        with _Kv4There(cache, stream):
+            return sparstar_kv4_write(cache, k, v, seqs, starts, counts, status)
     if k.dim() != 4:
         raise ValueError("k must be [n, Hkv, T, D]")
     n, _, T, _ = k.shape
     shape = (n, cache.Hkv, T, cache.D)
-    with _Kv4Call(cache, stream) as s:
-        _check(lib.sparstar_kv4_write(cache._struct, _kv4_tensor(cache, k, "k", k.dtype, shape),
-                                      _kv4_tensor(cache, v, "v", k.dtype, shape),
-                                      _DTYPE.get(k.dtype, -1), n, T,
-                                      _kv4_ints(cache, seqs, "seqs", n),
-                                      _kv4_ints(cache, starts, "starts", n),
-                                      _kv4_ints(cache, counts, "counts", n),
-                                      _kv4_status(cache, status), s),
-               "sparstar_kv4_write")
+    _check(lib.sparstar_kv4_write(cache._struct, _kv4_tensor(cache, k, "k", k.dtype, shape),
+                                  _kv4_tensor(cache, v, "v", k.dtype, shape),
+                                  _DTYPE.get(k.dtype, -1), n, T,
+                                  _kv4_ints(cache, seqs, "seqs", n),
+                                  _kv4_ints(cache, starts, "starts", n),
+                                  _kv4_ints(cache, counts, "counts", n),
+                                  _kv4_status(cache, status), _kv4_raw_stream(cache)),
+           "sparstar_kv4_write")
 
 
 def sparstar_kv4_read(cache: Kv4Cache, T: int, n: int = None, dtype=torch.bfloat16, seqs=None,
@@ -598,24 +605,28 @@ def sparstar_kv4_read(cache: Kv4Cache, T: int, n: int = None, dtype=torch.bfloat
     [n, Hkv, T, D].  Rows beyond counts are not written (buffers that the
     call allocates hold zeros there).  n, unless given, follows from seqs,
     starts, counts, k or v, and is every sequence without them."""
+    if _kv4_elsewhere(cache, stream):
+        with _Kv4There(cache, stream):
+            return sparstar_kv4_read(cache, T, n, dtype, seqs, starts, counts, k, v, status)
     if n is None:
         sizes = [t.shape[0] for t in (seqs, starts, counts, k, v) if t is not None]
         n = sizes[0] if sizes else cache.n_seqs
     shape = (n, cache.Hkv, T, cache.D)
     if k is not None or v is not None:
         dtype = (k if k is not None else v).dtype
-    with _Kv4Call(cache, stream) as s:
-        if k is None and v is None:
-            new = torch.empty if counts is None else torch.zeros
-            k, v = (new(shape, dtype=dtype, device=cache.device) for _ in range(2))
-        kp = None if k is None else _kv4_tensor(cache, k, "k", dtype, shape)
-        vp = None if v is None else _kv4_tensor(cache, v, "v", dtype, shape)
-        _check(lib.sparstar_kv4_read(cache._struct, kp, vp, _DTYPE.get(dtype, -1), n, T,
-                                     _kv4_ints(cache, seqs, "seqs", n),
-                                     _kv4_ints(cache, starts, "starts", n),
-                                     _kv4_ints(cache, counts, "counts", n),
-                                     _kv4_status(cache, status), s),
-               "sparstar_kv4_read")
+    elif _DTYPE.get(dtype, -1) < 0:
+        raise SparstarError(EDTYPE, "sparstar_kv4_read")
+    else:
+        new = torch.empty if counts is None else torch.zeros
+        k, v = (new(shape, dtype=dtype, device=cache.device) for _ in range(2))
+    kp = None if k is None else _kv4_tensor(cache, k, "k", dtype, shape)
+    vp = None if v is None else _kv4_tensor(cache, v, "v", dtype, shape)
+    _check(lib.sparstar_kv4_read(cache._struct, kp, vp, _DTYPE.get(dtype, -1), n, T,
+                                 _kv4_ints(cache, seqs, "seqs", n),
+                                 _kv4_ints(cache, starts, "starts", n),
+                                 _kv4_ints(cache, counts, "counts", n),
+                                 _kv4_status(cache, status), _kv4_raw_stream(cache)),
+           "sparstar_kv4_read")
     return k, v
 
 
@@ -633,48 +644,60 @@ def sparstar_kv4_attn(cache: Kv4Cache, q, seqs=None, tau: float = None, causal: 
     returns (out, lse).  ``work`` (uint8, its first KV4_WORK_ZEROS bytes zero
     before its first use): when not given, the cache keeps one a stream, and a
     call that is captured into a graph gets one of its own."""
+    if _kv4_elsewhere(cache, stream):
+        with _Kv4There(cache, stream):
+            return sparstar_kv4_attn(cache, q, seqs, tau, causal, kv_idx, kv_cnt, out, lse,
+                                     want_lse, work, status)
     if q.dim() != 4:
         raise ValueError("q must be [n, Hq, Lq, D]")
-    n, Hq, Lq, D = q.shape
-    dt = _DTYPE.get(q.dtype, -1)
+    shape = q.shape
+    n, Hq, Lq, D = shape
+    dtype = q.dtype
+    dt = _DTYPE.get(dtype, -1)
     if D != cache.D:
         raise ValueError("q has head dim %d, the cache %d" % (D, cache.D))
     if tau is None:
         tau = _TAU[D]
-    qp = _kv4_tensor(cache, q, "q", q.dtype, q.shape)
+    qp = _kv4_tensor(cache, q, "q", dtype, shape)
     if (kv_idx is None) != (kv_cnt is None):
         raise ValueError("kv_idx and kv_cnt go together")
-    max_sel, ip, cp = 0, None, None
+    max_sel, ip, cp = -1, None, None
     if kv_idx is not None:
         rows = (n, Hq, nblocks(Lq))
         max_sel = kv_idx.shape[-1]
         ip = _kv4_tensor(cache, kv_idx, "kv_idx", torch.int32, rows + (max_sel,))
         cp = _kv4_tensor(cache, kv_cnt, "kv_cnt", torch.int32, rows)
-    need = lib.sparstar_kv4_attn_work_bytes(n, Hq, cache.Hkv, Lq, D, dt, cache.max_pages,
-                                            -1 if kv_idx is None else max_sel)
-    if need < 0:
-        raise SparstarError(EDTYPE if dt < 0 else EINVAL, "sparstar_kv4_attn")
-    with _Kv4Call(cache, stream) as s:
-        op = lp = None
-        if out is None:
-            out = torch.empty_like(q)
-            op = out.data_ptr()
-        if lse is None and want_lse:
-            lse = torch.empty(n, Hq, Lq, dtype=torch.float32, device=cache.device)
-            lp = lse.data_ptr()
-        if op is None:
-            op = _kv4_tensor(cache, out, "out", q.dtype, q.shape)
-        if lp is None and lse is not None:
-            lp = _kv4_tensor(cache, lse, "lse", torch.float32, (n, Hq, Lq))
-        if work is None:
-            work = cache._attn_work(need, s)
-        elif work.dtype is not torch.uint8 or work.get_device() != cache.index \
-                or not work.is_contiguous():
-            raise ValueError("work must be contiguous uint8 on %s" % cache.device)
-        _check(lib.sparstar_kv4_attn(
-            cache._struct, qp, dt, n, Hq, Lq, _kv4_ints(cache, seqs, "seqs", n), tau,
-            int(bool(causal)), ip, cp, max_sel, op, lp, work.data_ptr(), work.numel(),
-            _kv4_status(cache, status), s), "sparstar_kv4_attn")
+    key = (n, Hq, Lq, dt, max_sel)
+    need = cache._need.get(key)
+    if need is None:
+        need = lib.sparstar_kv4_attn_work_bytes(n, Hq, cache.Hkv, Lq, D, dt, cache.max_pages,
+                                                max_sel)
+        if need < 0:
+            raise SparstarError(EDTYPE if dt < 0 else EINVAL, "sparstar_kv4_attn")
+        if len(cache._need) < 4096:
+            cache._need[key] = need
+    s = _kv4_raw_stream(cache)
+    if out is None:
+        out = torch.empty_like(q)
+        op = out.data_ptr()
+    else:
+        op = _kv4_tensor(cache, out, "out", dtype, shape)
+    if lse is not None:
+        lp = _kv4_tensor(cache, lse, "lse", torch.float32, shape[:3])
+    elif want_lse:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=cache.device)
+        lp = lse.data_ptr()
+    else:
+        lp = None
+    if work is None:
+        work = cache._attn_work(need, s)
+    elif work.dtype is not torch.uint8 or work.get_device() != cache.index \
+            or not work.is_contiguous():
+        raise ValueError("work must be contiguous uint8 on %s" % cache.device)
+    _check(lib.sparstar_kv4_attn(
+        cache._struct, qp, dt, n, Hq, Lq, _kv4_ints(cache, seqs, "seqs", n), tau,
+        1 if causal else 0, ip, cp, max_sel if max_sel > 0 else 0, op, lp, work.data_ptr(),
+        work.numel(), _kv4_status(cache, status), s), "sparstar_kv4_attn")
     return out, lse
 
 
