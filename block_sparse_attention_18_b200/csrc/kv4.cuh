@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "sparstar.h"
@@ -124,6 +125,24 @@ __device__ __forceinline__ int kv4_len(const Kv4 &c, int slot) {
     const int L = c.lens[slot];
     const int most = c.max_pages * kBlock;
     return L < 0 ? 0 : (L > most ? most : L);
+}
+
+// Launches a kernel that the one before it lets start early
+// (griddepcontrol.launch_dependents); it waits for that one's end itself.
+template <typename... Args>
+inline cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned block, size_t smem,
+                         cudaStream_t stream, Args... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace sparstar

@@ -82,7 +82,8 @@ struct Plan {
     int rows;       // rows of a stripe
     int pairs;      // query block pairs of a stripe
     int nqb;        // query blocks of a stripe
-    int splits;     // CTAs a unit; those behind its last page have nothing to do
+    int whole;      // units before this one run on one CTA each
+    int splits;     // CTAs of each other unit; those behind its last page do nothing
     int chunk;      // entries (pages or list entries) a CTA
     int32_t *chosen;  // unpacked first, without lists: the chunk that the lengths ask for
     bool halved;    // one query block a stripe: A and B are halves of its pages
@@ -175,6 +176,7 @@ __device__ Unit unit_of(const Kv4 &c, const Kv4Attn &a, const Plan &p, int unit)
     u.entries = max(u.count[0], u.count[1]);
     u.chunk = p.chosen ? __ldcg(p.chosen) : p.chunk;
     u.parts = max(1, (u.entries + u.chunk - 1) / u.chunk);
+    if (unit < p.whole) u.chunk = u.entries, u.parts = 1;
     return u;
 }
 
@@ -302,6 +304,7 @@ struct Unpack {
 // Unpacked first: one CTA a page and head of every sequence; four warps the
 // keys, four the values, 32 rows each.
 __global__ void __launch_bounds__(256) unpack_kernel(Kv4 c, Kv4Attn a, Plan p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (p.chosen && blockIdx.x == gridDim.x - 1) {  // one CTA behind the pages'
         choose_chunk(c, a, p);
         return;
@@ -353,8 +356,11 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
     // This CTA's pair of query blocks and part of their pages.
-    const int split = blockIdx.x % p.splits;
-    const Unit un = unit_of(c, a, p, blockIdx.x / p.splits);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (kPre) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tail = (int)blockIdx.x - p.whole;  // CTA of the split units
+    const int split = tail < 0 ? 0 : tail % p.splits;
+    const Unit un = unit_of(c, a, p, tail < 0 ? blockIdx.x : p.whole + tail / p.splits);
     const int stripe = un.stripe, qb0 = un.qb0, step_b = un.step_b, L = un.L;
     const int seq = un.seq, kh = un.kh;
     const bool lists = a.kv_cnt != nullptr;
@@ -867,7 +873,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                           wait_warp(bar_pv(x), (uint32_t)(nx - 1) & 1u, abort_flag, status);
         if (have) tc_fence_after();
         const int64_t out_row = (int64_t)stripe * p.rows + grow;
-        float *part = p.parts + (int64_t)blockIdx.x * kPartFloats;
+        float *part = p.parts + (int64_t)(joins ? tail : 0) * kPartFloats;
         float *part_o = part + 2 * kPartRows + (int64_t)(x * kBlock + row) * kHD;
         // A row without a weight (no token seen) gets 0.
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -925,12 +931,13 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
 __global__ void __launch_bounds__(256) many_join_kernel(Kv4 c, Kv4Attn a, Plan p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.halved ? kBlock : kPartRows;  // of a unit
-    const int unit = blockIdx.x / (rows / 8), r0 = blockIdx.x % (rows / 8) * 8 + warp;
-    const Unit u = unit_of(c, a, p, unit);
+    const int at = blockIdx.x / (rows / 8), r0 = blockIdx.x % (rows / 8) * 8 + warp;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Unit u = unit_of(c, a, p, p.whole + at);
     const int srow = u.qb0 * kBlock + r0;
     if (srow >= p.rows || (!p.halved && u.parts == 1)) return;
     const int n = p.halved ? 2 * u.parts : u.parts;  // <= 32
-    const float *first = p.parts + (int64_t)unit * p.splits * kPartFloats;
+    const float *first = p.parts + (int64_t)at * p.splits * kPartFloats;
     auto row_of = [&](int k, int &row) {  // record and row of part k
         row = p.halved ? (k & 1) * kBlock + r0 : r0;
         return first + (int64_t)(p.halved ? k >> 1 : k) * kPartFloats;
@@ -989,26 +996,35 @@ Shape shape_of(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq, bool lists) {
     return s;
 }
 
-// CTAs a unit, at most: as many as the scratch holds; where the device does
-// not choose, the number of least cost for units of equal length.
-int splits_of(int64_t units, int64_t tiles, bool device_chooses) {
-    int best = 1;
+// How a call's units are cut.  Where the device chooses the chunk: as many
+// CTAs a unit as the scratch holds.  Else, for units of equal length: whole
+// units in full waves first, the others split, as cheap as that gets.
+struct Cut {
+    int whole, splits;
+};
+Cut cut_of(int64_t units, int64_t tiles, bool device_chooses, bool halved) {
+    Cut best{0, 1};
     float least = 0.0f;
-    for (int s = 1; s <= kMaxSplits; ++s) {
-        if (s > 1 && (units * s > kMaxParts || tiles < 2 * s)) break;
-        const float cost = cost_of((float)(units * s), (float)ceil_div(tiles, s), 0.0f, s > 1,
-                                   true);
-        if (s == 1 || device_chooses || cost < least) best = s, least = cost;
+    for (int64_t whole = 0; whole <= units; whole += 148) {
+        if (whole > 0 && (halved || device_chooses)) break;
+        const float waves = (float)(whole / 148) * ((float)tiles + 4.0f);
+        for (int s = 1; s <= kMaxSplits; ++s) {
+            if (s > 1 && ((units - whole) * s > kMaxParts || tiles < 2 * s)) break;
+            const float cost = waves + cost_of((float)((units - whole) * s),
+                                               (float)ceil_div(tiles, s), 0.0f, s > 1, true);
+            if ((whole == 0 && s == 1) || device_chooses || cost < least)
+                best = Cut{(int)whole, s}, least = cost;
+        }
     }
     return best;
 }
 
-// Scratch of the splits of a call, whatever their number.
+// Scratch for the parts of a call, however it is cut.
 int64_t part_bytes(const Shape &s) {
     const int64_t u = s.units();
-    if (2 * u > kMaxParts) return s.halved() ? u * kPartFloats * 4 : 0;
-    const int64_t most = kMaxParts / u < kMaxSplits ? kMaxParts / u : kMaxSplits;
-    return u * most * kPartFloats * 4;
+    int64_t parts = u * kMaxSplits < kMaxParts ? u * kMaxSplits : kMaxParts;
+    if (s.halved() && parts < u) parts = u;  // every unit joins
+    return parts * kPartFloats * 4;
 }
 
 // Whether the pages are unpacked first.  That costs 22 ns a page and head
@@ -1047,7 +1063,8 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
     const int64_t entries = k.lists ? a.max_sel : c.max_pages;  // of a unit, at most
     p.halved = s.halved();
     const bool chooses = first && !k.lists && !p.halved && (a.n > 1 || a.causal);
-    p.splits = splits_of(s.units(), p.halved ? ceil_div(entries, 2) : entries, chooses);
+    const Cut cut = cut_of(s.units(), p.halved ? ceil_div(entries, 2) : entries, chooses, p.halved);
+    p.whole = cut.whole, p.splits = cut.splits;
     p.chunk = (int)ceil_div(entries > 0 ? entries : 1, p.splits);
     p.chosen = chooses && p.splits > 1
                    ? static_cast<int32_t *>(a.work) + SPARSTAR_KV4_WORK_ZEROS / 4
@@ -1060,15 +1077,19 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    if (first)
+    const int64_t tail = s.units() - p.whole;
+    const unsigned grid = (unsigned)(p.whole + tail * p.splits);
+    if (first) {
         unpack_kernel<<<(unsigned)((int64_t)a.n * c.max_pages * c.Hkv + (p.chosen ? 1 : 0)), 256,
                         0, stream>>>(c, a, p);
-    kernel<<<(unsigned)(s.units() * p.splits), first ? kThreads<true> : kThreads<false>,
-             kSmemBytes, stream>>>(mq, c, a, p);
-    if (p.halved || p.splits > 1)
-        many_join_kernel<<<(unsigned)(s.units() * (p.halved ? kBlock : kPartRows) / 8), 256, 0,
-                           stream>>>(c, a, p);
-    return cudaGetLastError();
+        e = launch_after(kernel, grid, kThreads<true>, kSmemBytes, stream, mq, c, a, p);
+    } else {
+        kernel<<<grid, kThreads<false>, kSmemBytes, stream>>>(mq, c, a, p);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess || (!p.halved && p.splits == 1) || tail == 0) return e;
+    return launch_after(many_join_kernel, (unsigned)(tail * (p.halved ? kBlock : kPartRows) / 8),
+                        256, 0, stream, c, a, p);
 }
 
 }  // namespace sparstar

@@ -399,23 +399,6 @@ __global__ void __launch_bounds__(kCopyThreads)
     }
 }
 
-// A kernel that the plan's lets start early; it waits for the plan's end.
-template <typename... Args>
-cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned block, size_t smem,
-                         cudaStream_t stream, Args... args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 cudaError_t launch_copy(const Kv4 &c, bool remap, int32_t *status, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(
         copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes);
