@@ -85,9 +85,11 @@ struct Plan {
     int whole;      // units before this one run on one CTA each
     int splits;     // CTAs of each other unit; those behind its last page do nothing
     int chunk;      // entries (pages or list entries) a CTA
-    int32_t *chosen;  // unpacked first, without lists: the chunk that the lengths ask for
+    int32_t *chosen;  // unpacked first, without lists: the chunk that the lengths ask for,
+                      // then the sequences in order
     bool halved;    // one query block a stripe: A and B are halves of its pages
     float sc;       // tau in log2 units, positive
+    int join_rows;  // rows a CTA of the joining kernel
     float *parts;
     uint8_t *tiles;  // unpacked first: [sequence][block][head] pairs of tiles
     int tile_blocks;
@@ -134,6 +136,9 @@ struct Walk {
     }
 };
 
+// Sequences that are put in order, units that are counted (choose_chunk).
+constexpr int kOrdered = 240, kChosenUnits = 1024;
+
 // A unit: a pair of query blocks of a stripe, and what they walk.
 struct Unit {
     int stripe, qb0, seq, kh, slot, L;
@@ -151,6 +156,11 @@ __device__ Unit unit_of(const Kv4 &c, const Kv4Attn &a, const Plan &p, int unit)
     const bool lists = a.kv_cnt != nullptr;
     const int per_seq = lists ? a.Hq : c.Hkv;
     u.seq = u.stripe / per_seq;
+    if (p.chosen && a.n <= kOrdered) {  // the longest sequences first
+        const int head = u.stripe - u.seq * per_seq;
+        u.seq = __ldcg(p.chosen + 1 + u.seq);
+        u.stripe = u.seq * per_seq + head;
+    }
     u.kh = lists ? u.stripe % per_seq / p.heads : u.stripe % per_seq;
     u.slot = kv4_slot(c, a.seqs, u.seq);
     u.L = u.slot >= 0 ? kv4_len(c, u.slot) : 0;
@@ -189,53 +199,62 @@ __host__ __device__ inline float cost_of(float ctas, float chunk, float steps, b
                                          bool equal) {
     const float own = chunk + (joins ? 8.0f : 4.0f);
     const float join = joins ? 3.0f + 0.02f * ctas : 0.0f;
-    if (equal) return ceilf(ctas / 148.0f) * own + join;
+    if (equal || ctas <= 148.0f) return ceilf(ctas / 148.0f) * own + join;
     const float packed = (steps + (joins ? 8.0f : 4.0f) * ctas) / 148.0f + 0.5f * chunk;
     return fmaxf(own, packed) + join;
 }
 
-// The chunk for the lengths at hand (no lists): of 1 .. splits chunks for the
-// longest unit, the number of least cost.  One CTA.
+// The chunk for the lengths at hand (no lists): of 32 between the longest
+// unit and its split into `splits`, the one of least cost; and the order of
+// the sequences, the longest first, so that no long unit starts last.  One
+// CTA of 256 threads.
 __device__ void choose_chunk(const Kv4 &c, const Kv4Attn &a, const Plan &p) {
-    __shared__ int32_t longest, ctas[kMaxSplits + 1];
+    constexpr int kTried = 32;
+    __shared__ int32_t longest, ctas[kTried], entries[kChosenUnits], lens[kOrdered];
     __shared__ unsigned long long steps;
     if (threadIdx.x == 0) longest = 1, steps = 0;
-    if (threadIdx.x <= kMaxSplits) ctas[threadIdx.x] = 0;
+    if (threadIdx.x < kTried) ctas[threadIdx.x] = 0;
     __syncthreads();
     // The key heads of a sequence have equal units: one stands for all.
-    const int units = a.n * p.pairs;
+    const int units = a.n * p.pairs;  // at most kChosenUnits
     Plan q = p;
     q.chosen = nullptr;
-    auto entries = [&](int k) {
-        return unit_of(c, a, q, k / p.pairs * c.Hkv * p.pairs + k % p.pairs).entries;
-    };
     for (int k = threadIdx.x; k < units; k += blockDim.x) {
-        const int e = entries(k);
-        atomicMax(&longest, e);
-        atomicAdd(&steps, (unsigned long long)e);
+        const Unit u = unit_of(c, a, q, k / p.pairs * c.Hkv * p.pairs + k % p.pairs);
+        entries[k] = u.entries;
+        if (k % p.pairs == 0 && u.seq < kOrdered) lens[u.seq] = u.L;
+        atomicMax(&longest, u.entries);
+        atomicAdd(&steps, (unsigned long long)u.entries);
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < units; k += blockDim.x) {
-        const int e = entries(k);
-        for (int s = 1; s <= p.splits; ++s) {
-            const int chunk = (longest + s - 1) / s;
-            atomicAdd(&ctas[s], max(1, (e + chunk - 1) / chunk));
+    const int tried = threadIdx.x & (kTried - 1);
+    const int least_chunk = max(2, (longest + p.splits - 1) / p.splits);
+    const int chunk = longest - max(0, longest - least_chunk) * tried / (kTried - 1);
+    int n = 0;
+    for (int k = threadIdx.x / kTried; k < units; k += blockDim.x / kTried)
+        n += max(1, (entries[k] + chunk - 1) / chunk);
+    atomicAdd(&ctas[tried], n);
+    if (a.n <= kOrdered)
+        for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
+            int before = 0;
+            for (int k = 0; k < a.n; ++k)
+                before += lens[k] > lens[i] || (lens[k] == lens[i] && k < i);
+            p.chosen[1 + before] = i;
         }
-    }
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < kTried) {
         const float all = (float)steps * c.Hkv;
         const bool equal = all >= 0.95f * (float)units * c.Hkv * longest;
-        int best = longest;
-        float least = 0.0f;
-        for (int s = 1; s <= p.splits; ++s) {
-            const int chunk = (longest + s - 1) / s;
-            if (s > 1 && chunk < 2) break;
-            const float cost =
-                cost_of((float)ctas[s] * c.Hkv, (float)chunk, all, s > 1, equal);
-            if (s == 1 || cost < least) best = chunk, least = cost;
+        float cost = cost_of((float)ctas[tried] * c.Hkv, (float)chunk, all, chunk < longest,
+                             equal);
+        int best = chunk;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {  // the least cost, then the larger chunk
+            const float other = __shfl_xor_sync(0xffffffffu, cost, o);
+            const int its = __shfl_xor_sync(0xffffffffu, best, o);
+            if (other < cost || (other == cost && its > best)) cost = other, best = its;
         }
-        *p.chosen = best;
+        if (threadIdx.x == 0) *p.chosen = best;
     }
 }
 
@@ -931,55 +950,61 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
 __global__ void __launch_bounds__(256) many_join_kernel(Kv4 c, Kv4Attn a, Plan p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.halved ? kBlock : kPartRows;  // of a unit
-    const int at = blockIdx.x / (rows / 8), r0 = blockIdx.x % (rows / 8) * 8 + warp;
+    const int at = blockIdx.x / (rows / p.join_rows);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Unit u = unit_of(c, a, p, p.whole + at);
-    const int srow = u.qb0 * kBlock + r0;
-    if (srow >= p.rows || (!p.halved && u.parts == 1)) return;
+    if (!p.halved && u.parts == 1) return;
     const int n = p.halved ? 2 * u.parts : u.parts;  // <= 32
     const float *first = p.parts + (int64_t)at * p.splits * kPartFloats;
-    auto row_of = [&](int k, int &row) {  // record and row of part k
-        row = p.halved ? (k & 1) * kBlock + r0 : r0;
-        return first + (int64_t)(p.halved ? k >> 1 : k) * kPartFloats;
-    };
-    float m = -INFINITY, l = 0.0f;
-    if (lane < n) {
-        int row;
-        const float *rec = row_of(lane, row);
-        m = rec[row], l = rec[kPartRows + row];
-    }
-    float top = m;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float f = m > -INFINITY ? ex2(m - top) : 0.0f;
-    float sum = f * l;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < n; k0 += 8) {
-        float4 x[8];
-        float w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            w[k] = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
-            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < p.join_rows / 8; ++i) {
+        const int r0 = blockIdx.x % (rows / p.join_rows) * p.join_rows + i * 8 + warp;
+        const int srow = u.qb0 * kBlock + r0;
+        if (srow >= p.rows) break;
+        auto row_of = [&](int k, int &row) {  // record and row of part k
+            row = p.halved ? (k & 1) * kBlock + r0 : r0;
+            return first + (int64_t)(p.halved ? k >> 1 : k) * kPartFloats;
+        };
+        float m = -INFINITY, l = 0.0f;
+        if (lane < n) {
             int row;
-            const float *rec = row_of(k0 + k, row);
-            // Parts without a seen token have stored nothing.
-            if (k0 + k < n && w[k] != 0.0f)
-                x[k] = *(reinterpret_cast<const float4 *>(rec + 2 * kPartRows + row * kHD) + lane);
+            const float *rec = row_of(lane, row);
+            m = rec[row], l = rec[kPartRows + row];
         }
+        float top = m;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            acc.x = fmaf(w[k], x[k].x, acc.x), acc.y = fmaf(w[k], x[k].y, acc.y);
-            acc.z = fmaf(w[k], x[k].z, acc.z), acc.w = fmaf(w[k], x[k].w, acc.w);
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float f = m > -INFINITY ? ex2(m - top) : 0.0f;
+        float sum = f * l;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < n; k0 += 8) {
+            float4 x[8];
+            float w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                w[k] = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                int row;
+                const float *rec = row_of(k0 + k, row);
+                // Parts without a seen token have stored nothing.
+                if (k0 + k < n && w[k] != 0.0f)
+                    x[k] = *(reinterpret_cast<const float4 *>(rec + 2 * kPartRows + row * kHD) +
+                             lane);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                acc.x = fmaf(w[k], x[k].x, acc.x), acc.y = fmaf(w[k], x[k].y, acc.y);
+                acc.z = fmaf(w[k], x[k].z, acc.z), acc.w = fmaf(w[k], x[k].w, acc.w);
+            }
         }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int64_t out_row = (int64_t)u.stripe * p.rows + srow;
+        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * kHD)[lane] =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        if (lane == 0 && a.lse) a.lse[out_row] = (top + log2f(sum)) * 0.6931471805599453f;
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t out_row = (int64_t)u.stripe * p.rows + srow;
-    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * kHD)[lane] =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (lane == 0 && a.lse) a.lse[out_row] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Stripes and pairs of query blocks of a call.
@@ -1062,7 +1087,8 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
     const bool first = unpack_first(s, k);
     const int64_t entries = k.lists ? a.max_sel : c.max_pages;  // of a unit, at most
     p.halved = s.halved();
-    const bool chooses = first && !k.lists && !p.halved && (a.n > 1 || a.causal);
+    const bool chooses = first && !k.lists && !p.halved && (a.n > 1 || a.causal) &&
+                         a.n * s.pairs <= kChosenUnits;
     const Cut cut = cut_of(s.units(), p.halved ? ceil_div(entries, 2) : entries, chooses, p.halved);
     p.whole = cut.whole, p.splits = cut.splits;
     p.chunk = (int)ceil_div(entries > 0 ? entries : 1, p.splits);
@@ -1088,7 +1114,11 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || (!p.halved && p.splits == 1) || tail == 0) return e;
-    return launch_after(many_join_kernel, (unsigned)(tail * (p.halved ? kBlock : kPartRows) / 8),
+    // Eight rows a CTA while these fit the GPU at once, then 32, which find
+    // their unit once.
+    const int64_t rows = tail * (p.halved ? kBlock : kPartRows);
+    p.join_rows = rows / 8 <= 148 * 8 ? 8 : 32;
+    return launch_after(many_join_kernel, (unsigned)(rows / p.join_rows),
                         256, 0, stream, c, a, p);
 }
 
