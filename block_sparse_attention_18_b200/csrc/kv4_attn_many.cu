@@ -1,53 +1,67 @@
 // Attention of many query rows over the paged 4-bit key/value cache, bf16
 // with head dim 128, on the 5th-generation tensor cores.
 //
-// The pipeline is attn_sm100.cu's: one CTA a pair of query blocks A and B
-// (128 rows each), whose scores share one TMEM buffer in turn, with P in
-// tensor memory as the A operand of O += P V.  What differs is where the
-// 128 x 128 tiles come from, in one of two ways:
+// The 128 x 128 tiles come from the pages in one of two ways:
 //
 //   unpacked first: a kernel of its own dequantises every page once (exactly,
 //     to bf16) into scratch, as the 32 KB tiles in the 128-byte swizzle that
 //     the MMAs read from shared memory, and the attention kernel's producer
 //     fetches them with one bulk copy each.  64 KB a page and head are
 //     written and, mostly from L2, read again: right where many query blocks
-//     read the same pages.
-//   unpacked in place: three warps of the attention kernel read the packed
+//     read the same pages.  The pipeline is attn_sm100.cu's: one CTA a pair
+//     of query blocks A and B (128 rows each), whose scores share one TMEM
+//     buffer in turn, with P in tensor memory as the A operand of O += P V.
+//     Without block lists A and B are neighbouring blocks of the rows that
+//     share a key head (the heads of a group lie one behind the other in q)
+//     and walk the same pages: a tile serves 256 rows.  With lists each block
+//     walks its own.
+//   unpacked in place: seven warps of the attention kernel read the packed
 //     pages into registers (the next tile's words and the page of the one
 //     after are on their way while this one is unpacked), dequantise them and
 //     write them to the ring.  Only the packed bytes cross HBM: right for few
-//     query blocks and long caches.  One warp issues both products, polling
-//     for whichever is ready, so that twelve warps keep 168 registers each (a
-//     row of scores stays in registers).
+//     query blocks and long caches.  One query block a CTA, with two TMEM
+//     buffers for its scores; one warp issues both products, polling for
+//     whichever is ready.  Twelve warps keep 168 registers each (a row of
+//     scores stays in registers).  With three unpacking warps beside two
+//     blocks' softmax, unpacking was the bound: 2.4 us a page and block
+//     against 1.2 now.
 //
-// Values lie channel by channel in a page, so both operands are K-major.
-// Without block lists A and B are neighbouring blocks of the rows that share
-// a key head (the heads of a group lie one behind the other in q) and walk
-// the same pages: a tile serves 256 rows.  With lists each block walks its
-// own.  A stripe of one block runs as both A and B, each on half of the pages
-// (one block alone would wait for its own softmax).  Few CTAs (short stripes,
-// long caches) split the pages among several; a kernel of its own joins the
-// results, in order.
+// Values lie channel by channel in a page, so both operands are K-major.  Few
+// CTAs (short stripes, long caches) split the pages among several; a kernel
+// of its own joins the results, in order.
 #include "kv4.cuh"
 #include "sm100.cuh"
 
 namespace sparstar {
 namespace {
 
-constexpr int kSoftmaxThreads = 256;  // warps 0-3 block A, 4-7 block B
-// Unpacked first: warp 8 copies, 9 issues S = Q K^T, 10 O += P V.  Unpacked
-// in place: warps 8-10 unpack, 11 issues both.
+// Query blocks a CTA.
+template <bool kPre>
+constexpr int kBlocks = kPre ? 2 : 1;
+// Unpacked first: warps 0-3 softmax of block A, 4-7 of B, 8 copies, 9 issues
+// S = Q K^T, 10 O += P V.  In place: 0-3 softmax, 4-10 unpack, 11 issues both.
 template <bool kPre>
 constexpr int kThreads = kPre ? 352 : 384;
 template <bool kPre>
 constexpr int kLoadWarp = kPre ? 8 : 11;   // Q, barriers
 template <bool kPre>
 constexpr int kMmaWarp = kPre ? 9 : 11;    // TMEM, S = Q K^T
-constexpr int kPvWarp = 10, kUnpackWarp = 8, kUnpackWarps = 3;
+constexpr int kPvWarp = 10, kUnpackWarp = 4, kUnpackWarps = 7;
+constexpr int kUnpackStrips = 3;  // of 16 strips of eight rows, a warp at most
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0;
-__host__ __device__ constexpr uint32_t col_p(int x) { return x ? 192u : 128u; }
-__host__ __device__ constexpr uint32_t col_o(int x) { return x ? 384u : 256u; }
+// TMEM columns: scores of step j, P and O of block x.
+template <bool kPre>
+__device__ constexpr uint32_t col_s(int j) {
+    return kPre ? 0u : (j & 1) * 128u;
+}
+template <bool kPre>
+__device__ constexpr uint32_t col_p(int x) {
+    return kPre ? (x ? 192u : 128u) : 256u;
+}
+template <bool kPre>
+__device__ constexpr uint32_t col_o(int x) {
+    return kPre ? (x ? 384u : 256u) : 384u;
+}
 
 constexpr int kOffQ = 0;
 constexpr int kOffStage = 2 * kTileBytes;
@@ -56,8 +70,8 @@ struct Bars {
     uint64_t q_full;
     uint64_t st_full[kStages][2];  // [stage][use & 1], see ring_parity
     uint64_t st_empty[kStages];
-    uint64_t s_full[2];
-    uint64_t s_free;
+    uint64_t s_full[2];  // unpacked first: of block A, B; in place: of the two buffers
+    uint64_t s_free[2];  // unpacked first: [0]; in place: of the two buffers
     uint64_t p_full[2][2];
     uint64_t pv_done[2];
     uint64_t drain;
@@ -69,9 +83,8 @@ constexpr int kSmemBytes = kOffBar + (int)sizeof(Bars) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 constexpr uint32_t kIdesc = make_idesc(false);  // both operands K-major
 
-// Partial results of a CTA's 256 rows: maxima, sums, accumulators.
-constexpr int kPartRows = 2 * kBlock;
-constexpr int kPartFloats = kPartRows * (kHD + 2);
+// Partial results of a CTA's rows, up to 256: maxima, sums, accumulators.
+constexpr int kPartFloats = kBlock * (kHD + 2);  // a query block
 constexpr int kMaxParts = 4 * 148;  // units x splits, bounds the scratch
 constexpr int kMaxSplits = 16;
 // Scratch: the other kernel's zeros, the chosen chunk, the parts, the tiles.
@@ -80,14 +93,14 @@ constexpr int kHeadBytes = SPARSTAR_KV4_WORK_ZEROS + 1024;
 struct Plan {
     int heads;      // query heads a key head
     int rows;       // rows of a stripe
-    int pairs;      // query block pairs of a stripe
+    int blocks;     // query blocks a unit: 2 unpacked first, 1 in place
+    int per;        // units of a stripe
     int nqb;        // query blocks of a stripe
     int whole;      // units before this one run on one CTA each
     int splits;     // CTAs of each other unit; those behind its last page do nothing
     int chunk;      // entries (pages or list entries) a CTA
     int32_t *chosen;  // unpacked first, without lists: the chunk that the lengths ask for,
                       // then the sequences in order
-    bool halved;    // one query block a stripe: A and B are halves of its pages
     float sc;       // tau in log2 units, positive
     int join_rows;  // rows a CTA of the joining kernel
     float *parts;
@@ -108,10 +121,6 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ void softmax_barrier() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
-}
-
 // The pages one query block walks.
 struct Walk {
     const int32_t *list;   // block list, or null: every block
@@ -139,10 +148,9 @@ struct Walk {
 // Sequences that are put in order, units that are counted (choose_chunk).
 constexpr int kOrdered = 240, kChosenUnits = 1024;
 
-// A unit: a pair of query blocks of a stripe, and what they walk.
+// A unit: one or two query blocks of a stripe, and what they walk.
 struct Unit {
     int stripe, qb0, seq, kh, slot, L;
-    int step_b;      // block B is qb0 + step_b
     int visible[2];  // blocks that some row of the query block sees
     int count[2];    // entries it walks
     int entries, chunk, parts;
@@ -150,9 +158,8 @@ struct Unit {
 // The last blocks of a stripe see most under a causal mask: they come first.
 __device__ Unit unit_of(const Kv4 &c, const Kv4Attn &a, const Plan &p, int unit) {
     Unit u;
-    u.stripe = unit / p.pairs;
-    u.qb0 = 2 * (p.pairs - 1 - unit % p.pairs);
-    u.step_b = p.halved ? 0 : 1;
+    u.stripe = unit / p.per;
+    u.qb0 = p.blocks * (p.per - 1 - unit % p.per);
     const bool lists = a.kv_cnt != nullptr;
     const int per_seq = lists ? a.Hq : c.Hkv;
     u.seq = u.stripe / per_seq;
@@ -166,8 +173,8 @@ __device__ Unit unit_of(const Kv4 &c, const Kv4Attn &a, const Plan &p, int unit)
     u.L = u.slot >= 0 ? kv4_len(c, u.slot) : 0;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        const int first = (u.qb0 + x * u.step_b) * kBlock;
-        const int last = min(first + kBlock, p.rows) - 1;
+        const int first = (u.qb0 + x) * kBlock;
+        const int last = x < p.blocks ? min(first + kBlock, p.rows) - 1 : first - 1;
         int seen = u.L;  // by the row that sees most
         if (a.causal) {
             const int in = first % a.Lq + last - first;
@@ -216,13 +223,13 @@ __device__ void choose_chunk(const Kv4 &c, const Kv4Attn &a, const Plan &p) {
     if (threadIdx.x < kTried) ctas[threadIdx.x] = 0;
     __syncthreads();
     // The key heads of a sequence have equal units: one stands for all.
-    const int units = a.n * p.pairs;  // at most kChosenUnits
+    const int units = a.n * p.per;  // at most kChosenUnits
     Plan q = p;
     q.chosen = nullptr;
     for (int k = threadIdx.x; k < units; k += blockDim.x) {
-        const Unit u = unit_of(c, a, q, k / p.pairs * c.Hkv * p.pairs + k % p.pairs);
+        const Unit u = unit_of(c, a, q, k / p.per * c.Hkv * p.per + k % p.per);
         entries[k] = u.entries;
-        if (k % p.pairs == 0 && u.seq < kOrdered) lens[u.seq] = u.L;
+        if (k % p.per == 0 && u.seq < kOrdered) lens[u.seq] = u.L;
         atomicMax(&longest, u.entries);
         atomicAdd(&steps, (unsigned long long)u.entries);
     }
@@ -380,27 +387,26 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
     const int tail = (int)blockIdx.x - p.whole;  // CTA of the split units
     const int split = tail < 0 ? 0 : tail % p.splits;
     const Unit un = unit_of(c, a, p, tail < 0 ? blockIdx.x : p.whole + tail / p.splits);
-    const int stripe = un.stripe, qb0 = un.qb0, step_b = un.step_b, L = un.L;
+    const int stripe = un.stripe, qb0 = un.qb0, L = un.L;
     const int seq = un.seq, kh = un.kh;
     const bool lists = a.kv_cnt != nullptr;
     if (un.slot < 0 && threadIdx.x == 0) kv4_flag(status, SPARSTAR_STATUS_BAD_INDEX);
     if (split >= un.parts) return;
-    const bool joins = p.halved || un.parts > 1;  // the result goes to `parts`
+    const bool joins = un.parts > 1;  // the result goes to `parts`
     Walk walk[2];
     {
         const int lo = split * un.chunk, hi = min(lo + un.chunk, un.entries);
-        const int mid = (lo + hi + 1) / 2;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             Walk &w = walk[x];
-            w.list = lists ? a.kv_idx + ((int64_t)stripe * p.nqb + qb0 + x * step_b) * a.max_sel
+            w.list = lists ? a.kv_idx + ((int64_t)stripe * p.nqb + qb0 + x) * a.max_sel
                            : nullptr;
             w.table = c.table + (int64_t)(un.slot >= 0 ? un.slot : 0) * c.max_pages;
             w.blocks = (L + kBlock - 1) / kBlock;
             w.n_pages = c.n_pages;
             w.visible = un.visible[x];
-            w.lo = p.halved && x == 1 ? mid : lo;
-            w.hi = max(w.lo, min(p.halved && x == 0 ? mid : hi, un.count[x]));
+            w.lo = lo;
+            w.hi = max(lo, min(hi, un.count[x]));
         }
     }
 
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
     };
     auto bar_empty = [&](int s) { return smem_addr(&bars->st_empty[s]); };
     auto bar_s = [&](int x) { return smem_addr(&bars->s_full[x]); };
-    const uint32_t bar_sfree = smem_addr(&bars->s_free);
+    auto bar_sfree = [&](int b) { return smem_addr(&bars->s_free[b]); };
     auto bar_p = [&](int x, int h) { return smem_addr(&bars->p_full[x][h]); };
     auto bar_pv = [&](int x) { return smem_addr(&bars->pv_done[x]); };
     const uint32_t bar_drain = smem_addr(&bars->drain);
@@ -423,10 +429,10 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 mbar_init(smem_addr(&bars->st_full[s][1]), kPre ? 1 : kUnpackWarps);
                 mbar_init(bar_empty(s), 1);
             }
-            mbar_init(bar_sfree, kSoftmaxThreads / 2);
             for (int x = 0; x < 2; ++x) {
                 mbar_init(bar_s(x), 1);
-                for (int h = 0; h < 2; ++h) mbar_init(bar_p(x, h), kSoftmaxThreads / 2);
+                mbar_init(bar_sfree(x), kBlock);
+                for (int h = 0; h < 2; ++h) mbar_init(bar_p(x, h), kBlock);
                 mbar_init(bar_pv(x), 1);
             }
             mbar_init(bar_drain, kPre ? 2 : 1);
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < kBlocks<kPre>; ++x) {
             int nv = 0;
             bool bad = false;
             for (int t = walk[x].lo + lane; t < walk[x].hi; t += 32) {
@@ -461,16 +467,16 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
-    const int nA = bars->n_valid[0], nB = bars->n_valid[1];
+    const int nA = bars->n_valid[0], nB = kPre ? bars->n_valid[1] : 0;
     const int nmax = nA > nB ? nA : nB;
     // Ring streams: the tiles of A and of B, or one stream for both.
-    const bool apart = lists || p.halved;
+    const bool apart = lists;
     const int sA = apart ? nA : nmax, sB = apart ? nB : 0;
     auto k_slot = [&](int x, int j) { return slot_k(apart ? x : 0, j, sA, sB); };
     auto v_slot = [&](int x, int j) { return slot_v(apart ? x : 0, j, sA, sB); };
 
     // The stream whose pages A and B share is the longer one.
-    const Walk wa = apart || nA >= nB ? walk[0] : walk[1], wb = walk[1];
+    const Walk wa = !kPre || apart || nA >= nB ? walk[0] : walk[1], wb = walk[1];
     // Tiles in ring order: bit 0 values, bit 1 stream B; -1 after the last.
     int step = -1, phase = 0;
     auto next_tile = [&]() {
@@ -501,14 +507,15 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         mbar_expect_tx(bar_q, nq * kTileBytes);
         for (int x = 0; x < nq; ++x) {
             const uint32_t sQ = base + kOffQ + x * kTileBytes;
-            const int row = (qb0 + x * step_b) * kBlock;
+            const int row = (qb0 + x) * kBlock;
             tma_load_3d(sQ, &tmQ, bar_q, 0, row, stripe, pol);
             tma_load_3d(sQ + kPanelBytes, &tmQ, bar_q, 64, row, stripe, pol);
         }
     };
     const uint64_t dQ0 = desc_k_major(base + kOffQ);
     const uint64_t dQ1 = desc_k_major(base + kOffQ + kTileBytes);
-    // S = Q_x K^T of ring slot e; a shared tile is free after its last reader.
+    // S = Q_x K^T of step j, ring slot e; a shared tile is free after its last
+    // reader.
     auto issue_qk = [&](int x, int j, int e) {
         const int stage = e % kStages;
         const uint64_t dK = desc_k_major(base + kOffStage + stage * kTileBytes);
@@ -519,10 +526,10 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
 #pragma unroll
             for (int kk = 0; kk < kHD / 16; ++kk) {
                 const uint64_t o = (uint64_t)(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4);
-                mma_ss(tmem + kColS, dQ + o, dK + o, kIdesc, kk > 0 ? 1u : 0u);
+                mma_ss(tmem + col_s<kPre>(j), dQ + o, dK + o, kIdesc, kk > 0 ? 1u : 0u);
             }
             if (frees) mma_commit(bar_empty(stage));
-            mma_commit(bar_s(x));
+            mma_commit(bar_s(kPre ? x : j & 1));
         }
         __syncwarp();
     };
@@ -536,7 +543,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
 #pragma unroll
             for (int kq = 0; kq < 4; ++kq) {
                 const uint64_t o = (uint64_t)((h * kPanelBytes + kq * 32) >> 4);
-                mma_ts(tmem + col_o(x), tmem + col_p(x) + 8u * (4 * h + kq), dV + o, kIdesc,
+                mma_ts(tmem + col_o<kPre>(x), tmem + col_p<kPre>(x) + 8u * (4 * h + kq), dV + o, kIdesc,
                        h > 0 || kq > 0 || j > 0 ? 1u : 0u);
             }
             if (h == 1) {
@@ -586,7 +593,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 const int e = k_slot(x, j);
                 ok = wait_warp(bar_full(e), ring_parity(e), abort_flag, status) &&
                      (n == 0 ||
-                      wait_warp(bar_sfree, (uint32_t)(n - 1) & 1u, abort_flag, status));
+                      wait_warp(bar_sfree(0), (uint32_t)(n - 1) & 1u, abort_flag, status));
                 if (!ok) break;
                 issue_qk(x, j, e);
                 ++n;
@@ -627,36 +634,28 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         auto ready = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_poll(bar, parity));
         };
-        // The next S (block qx of step qj, the n-th) and the next half of O.
-        int qx = nA > 0 ? 0 : 1, qj = 0, n = 0, vx = qx, vj = 0, vh = 0;
-        auto after = [&](int &x, int &j) {  // the block after x of step j
-            do {
-                if (x == 0) x = 1;
-                else x = 0, ++j;
-            } while (j < nmax && j >= (x == 0 ? nA : nB));
-        };
+        // The next S (step qj) and the next half of O (step vj).
+        int qj = 0, vj = 0, vh = 0;
         uint64_t idle = globaltimer();
-        while (ok && (qj < nmax || vj < nmax)) {
+        while (ok && vj < nA) {
             bool moved = false;
-            if (qj < nmax) {
-                const int e = k_slot(qx, qj);
+            if (qj < nA) {
+                const int e = k_slot(0, qj);
+                // The buffer's scores before these have been read.
                 if (ready(bar_full(e), ring_parity(e)) &&
-                    (n == 0 || ready(bar_sfree, (uint32_t)(n - 1) & 1u))) {
-                    issue_qk(qx, qj, e);
-                    ++n;
-                    after(qx, qj);
+                    (qj < 2 || ready(bar_sfree(qj & 1), (uint32_t)((qj >> 1) - 1) & 1u))) {
+                    issue_qk(0, qj, e);
+                    ++qj;
                     moved = true;
                 }
             }
-            if (vj < nmax) {
-                const int e = v_slot(vx, vj);
-                if (ready(bar_p(vx, vh), (uint32_t)vj & 1u) &&
-                    (vh > 0 || ready(bar_full(e), ring_parity(e)))) {
-                    issue_pv(vx, vj, vh, e);
-                    vh ^= 1;
-                    if (vh == 0) after(vx, vj);
-                    moved = true;
-                }
+            const int e = v_slot(0, vj);
+            if (ready(bar_p(0, vh), (uint32_t)vj & 1u) &&
+                (vh > 0 || ready(bar_full(e), ring_parity(e)))) {
+                issue_pv(0, vj, vh, e);
+                vh ^= 1;
+                if (vh == 0) ++vj;
+                moved = true;
             }
             if (moved) {
                 idle = globaltimer();
@@ -685,20 +684,20 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         __syncwarp();
     } else if (!kPre && warp >= kUnpackWarp) {
         // ------------------------------------------------- unpacking warps
-        // 16 strips of eight rows: 0-5, 6-10, 11-15, in two groups of channels
-        // at most (a group is four strips).
+        // 16 strips of eight rows: 0-2, 3-5, then two each; in two groups of
+        // channels at most (a group is four strips).
         const int w = warp - kUnpackWarp, g = lane & 3, q = lane >> 2;
-        const int strip0 = w == 0 ? 0 : 5 * w + 1, strips = w == 0 ? 6 : 5;
+        const int strip0 = w < 2 ? 3 * w : 2 * w + 2, strips = w < 2 ? 3 : 2;
         const Unpack u(lane);
         const int64_t head = (int64_t)kh * kv4_page_bytes(kHD);
         const int64_t page_bytes = (int64_t)c.Hkv * kv4_page_bytes(kHD);
-        uint4 code[6], vs[2][2];
-        uint32_t ks[6];
+        uint4 code[kUnpackStrips], vs[2][2];
+        uint32_t ks[kUnpackStrips];
         auto load = [&](int tile, int page) {
             const uint8_t *half = c.pages + page * page_bytes + head +
                                   (tile & 1) * kv4_half_bytes(kHD);
 #pragma unroll
-            for (int i = 0; i < 6; ++i)
+            for (int i = 0; i < kUnpackStrips; ++i)
                 if (i < strips)
                     code[i] = __ldg(reinterpret_cast<const uint4 *>(half) +
                                     ((strip0 + i) * 8 + q) * 4 + g);
@@ -707,12 +706,12 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint4 *sv = reinterpret_cast<const uint4 *>(
-                        s + ((strip0 >> 2) + k) * kBlock + 32 * g);
+                        s + min((strip0 >> 2) + k, 3) * kBlock + 32 * g);
                     vs[k][0] = __ldg(sv), vs[k][1] = __ldg(sv + 1);
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 6; ++i)
+                for (int i = 0; i < kUnpackStrips; ++i)
                     if (i < strips) ks[i] = __ldg(s + ((strip0 + i) * 8 + q) * 4 + g);
             }
         };
@@ -725,10 +724,10 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         int tile1 = next_tile();
         if (tile1 >= 0) find(tile1, page1);
         while (tile >= 0) {
-            uint4 now[6], vn[2][2];
-            uint32_t kn[6];
+            uint4 now[kUnpackStrips], vn[2][2];
+            uint32_t kn[kUnpackStrips];
 #pragma unroll
-            for (int i = 0; i < 6; ++i) now[i] = code[i], kn[i] = ks[i];
+            for (int i = 0; i < kUnpackStrips; ++i) now[i] = code[i], kn[i] = ks[i];
 #pragma unroll
             for (int k = 0; k < 2; ++k) vn[k][0] = vs[k][0], vn[k][1] = vs[k][1];
             const int tile2 = next_tile();
@@ -749,13 +748,13 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 Unpack::Pairs pairs;
                 u.pairs(vn[0][0], vn[0][1], pairs);
 #pragma unroll
-                for (int i = 0; i < 6; ++i) {
+                for (int i = 0; i < kUnpackStrips; ++i) {
                     if (i == in_first) u.pairs(vn[1][0], vn[1][1], pairs);
                     if (i < strips) u.values(now[i], pairs, strip0 + i, put);
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 6; ++i)
+                for (int i = 0; i < kUnpackStrips; ++i)
                     if (i < strips) u.keys(now[i], kn[i], strip0 + i, put);
             }
             // The MMAs read through the async proxy.
@@ -771,11 +770,11 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const uint32_t colO = col_o(x), colP = col_p(x);
+        const uint32_t colO = col_o<kPre>(x), colP = col_p<kPre>(x);
         const int nx = x == 0 ? nA : nB;
         const float sc = p.sc;
-        const Walk wx = x == 0 ? walk[0] : walk[1];
-        const int grow = (qb0 + x * step_b) * kBlock + row;  // of the stripe
+        const Walk wx = !kPre || x == 0 ? walk[0] : walk[1];
+        const int grow = (qb0 + x) * kBlock + row;  // of the stripe
         const bool real = grow < p.rows;
         // Tokens the row sees; a tile is masked where a row sees part of it.
         const int seen = a.causal ? L - a.Lq + 1 + grow % a.Lq : L;
@@ -787,7 +786,8 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             int kb, page;
             if (plain) kb = wx.list ? __ldg(wx.list + wx.lo + j) : wx.lo + j;
             else kb = wx.next(cur, page);
-            if (!wait_warp(bar_s(x), (uint32_t)j & 1u, abort_flag, status)) {
+            const int buffer = kPre ? x : j & 1;
+            if (!wait_warp(bar_s(buffer), (uint32_t)(kPre ? j : j >> 1) & 1u, abort_flag, status)) {
                 ok = false;
                 break;
             }
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             {
                 uint32_t r[4][32];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(tmem + lane_base + kColS + 32 * q, r[q]);
+                for (int q = 0; q < 4; ++q) tmem_ld32(tmem + lane_base + col_s<kPre>(j) + 32 * q, r[q]);
                 tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) reg_fence(r[q]);
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                     for (int u = 0; u < 32; ++u) s[32 * q + u] = __uint_as_float(r[q][u]);
             }
             tc_fence_before();
-            mbar_arrive(bar_sfree);
+            mbar_arrive(bar_sfree(kPre ? 0 : buffer));
             const int valid = seen - kb * kBlock;
             if (__any_sync(0xffffffffu, valid < kBlock)) {
 #pragma unroll
@@ -892,8 +892,8 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                           wait_warp(bar_pv(x), (uint32_t)(nx - 1) & 1u, abort_flag, status);
         if (have) tc_fence_after();
         const int64_t out_row = (int64_t)stripe * p.rows + grow;
-        float *part = p.parts + (int64_t)(joins ? tail : 0) * kPartFloats;
-        float *part_o = part + 2 * kPartRows + (int64_t)(x * kBlock + row) * kHD;
+        float *part = p.parts + (int64_t)(joins ? tail * kBlocks<kPre> + x : 0) * kPartFloats;
+        float *part_o = part + 2 * kBlock + (int64_t)row * kHD;
         // A row without a weight (no token seen) gets 0.
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -928,8 +928,8 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             }
         }
         if (joins) {
-            part[x * kBlock + row] = m_ref;
-            part[kPartRows + x * kBlock + row] = l;
+            part[row] = m_ref;
+            part[kBlock + row] = l;
         } else if (real && a.lse && (nx == 0 || have)) {
             a.lse[out_row] = (m_ref + log2f(l)) * 0.6931471805599453f;
         }
@@ -949,27 +949,26 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
 // All maxima and sums at once (one a lane), then eight accumulators a step.
 __global__ void __launch_bounds__(256) many_join_kernel(Kv4 c, Kv4Attn a, Plan p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = p.halved ? kBlock : kPartRows;  // of a unit
+    const int rows = p.blocks * kBlock;  // of a unit
     const int at = blockIdx.x / (rows / p.join_rows);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Unit u = unit_of(c, a, p, p.whole + at);
-    if (!p.halved && u.parts == 1) return;
-    const int n = p.halved ? 2 * u.parts : u.parts;  // <= 32
-    const float *first = p.parts + (int64_t)at * p.splits * kPartFloats;
+    if (u.parts == 1) return;
+    const int n = u.parts;  // <= kMaxSplits
+    const float *first = p.parts + (int64_t)at * p.splits * p.blocks * kPartFloats;
 #pragma unroll 2
     for (int i = 0; i < p.join_rows / 8; ++i) {
         const int r0 = blockIdx.x % (rows / p.join_rows) * p.join_rows + i * 8 + warp;
         const int srow = u.qb0 * kBlock + r0;
         if (srow >= p.rows) break;
-        auto row_of = [&](int k, int &row) {  // record and row of part k
-            row = p.halved ? (k & 1) * kBlock + r0 : r0;
-            return first + (int64_t)(p.halved ? k >> 1 : k) * kPartFloats;
+        const int row = r0 % kBlock;
+        auto record = [&](int k) {
+            return first + ((int64_t)k * p.blocks + r0 / kBlock) * kPartFloats;
         };
         float m = -INFINITY, l = 0.0f;
         if (lane < n) {
-            int row;
-            const float *rec = row_of(lane, row);
-            m = rec[row], l = rec[kPartRows + row];
+            const float *rec = record(lane);
+            m = rec[row], l = rec[kBlock + row];
         }
         float top = m;
 #pragma unroll
@@ -986,11 +985,10 @@ __global__ void __launch_bounds__(256) many_join_kernel(Kv4 c, Kv4Attn a, Plan p
             for (int k = 0; k < 8; ++k) {
                 w[k] = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
                 x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                int row;
-                const float *rec = row_of(k0 + k, row);
                 // Parts without a seen token have stored nothing.
                 if (k0 + k < n && w[k] != 0.0f)
-                    x[k] = *(reinterpret_cast<const float4 *>(rec + 2 * kPartRows + row * kHD) +
+                    x[k] = *(reinterpret_cast<const float4 *>(record(k0 + k) + 2 * kBlock +
+                                                              row * kHD) +
                              lane);
             }
 #pragma unroll
@@ -1007,38 +1005,40 @@ __global__ void __launch_bounds__(256) many_join_kernel(Kv4 c, Kv4Attn a, Plan p
     }
 }
 
-// Stripes and pairs of query blocks of a call.
+// Stripes of a call, and the units of one with `blocks` query blocks each.
 struct Shape {
-    int64_t stripes, rows, pairs;
-    int64_t units() const { return stripes * pairs; }
-    bool halved() const { return rows <= kBlock; }
+    int64_t stripes, rows, blocks, per;
+    int64_t units() const { return stripes * per; }
 };
-Shape shape_of(int64_t n, int64_t Hq, int64_t Hkv, int64_t Lq, bool lists) {
+Shape shape_of(const Kv4Shape &k, int64_t blocks) {
     Shape s;
-    s.stripes = n * (lists ? Hq : Hkv);
-    s.rows = lists ? Lq : Hq / Hkv * Lq;
-    s.pairs = ceil_div(s.rows, kPartRows);
+    s.stripes = k.n * (k.lists ? k.Hq : k.Hkv);
+    s.rows = k.lists ? k.Lq : k.Hq / k.Hkv * k.Lq;
+    s.blocks = blocks;
+    s.per = ceil_div(s.rows, blocks * kBlock);
     return s;
 }
 
 // How a call's units are cut.  Where the device chooses the chunk: as many
 // CTAs a unit as the scratch holds.  Else, for units of equal length: whole
 // units in full waves first, the others split, as cheap as that gets.
+constexpr float kInPlaceStep = 0.7f;
+constexpr int kInPlaceBlocks = 4;
 struct Cut {
     int whole, splits;
 };
 // `step`: what a step takes, in the steps of cost_of.
-Cut cut_of(int64_t units, int64_t tiles, float step, bool device_chooses, bool halved) {
+Cut cut_of(int64_t units, int64_t tiles, float step, bool device_chooses) {
     Cut best{0, 1};
     float least = 0.0f;
     for (int64_t whole = 0; whole <= units; whole += 148) {
-        if (whole > 0 && (halved || device_chooses)) break;
+        if (whole > 0 && device_chooses) break;
         const float waves = (float)(whole / 148) * (step * (float)tiles + 4.0f);
         for (int s = 1; s <= kMaxSplits; ++s) {
             if (s > 1 && ((units - whole) * s > kMaxParts || tiles < 2 * s)) break;
             const float cost =
                 waves + cost_of((float)((units - whole) * s),
-                                step * (float)ceil_div(tiles, s), 0.0f, s > 1 || halved, true);
+                                step * (float)ceil_div(tiles, s), 0.0f, s > 1, true);
             if ((whole == 0 && s == 1) || device_chooses || cost < least)
                 best = Cut{(int)whole, s}, least = cost;
         }
@@ -1048,54 +1048,48 @@ Cut cut_of(int64_t units, int64_t tiles, float step, bool device_chooses, bool h
 
 // Scratch for the parts of a call, however it is cut.
 int64_t part_bytes(const Shape &s) {
-    const int64_t u = s.units();
-    int64_t parts = u * kMaxSplits < kMaxParts ? u * kMaxSplits : kMaxParts;
-    if (s.halved() && parts < u) parts = u;  // every unit joins
-    return parts * kPartFloats * 4;
+    const int64_t parts = s.units() * kMaxSplits;
+    return (parts < kMaxParts ? parts : kMaxParts) * s.blocks * kPartFloats * 4;
 }
 
 // Whether the pages are unpacked first.  That costs 22 ns a page and head
-// (measured, over the whole GPU); unpacking in place makes a visit of a page
-// by a pair of blocks 9 ns longer, by a block with its own list 12 ns.
-bool unpack_first(const Shape &s, const Kv4Shape &k) {
+// (measured, over the whole GPU) and makes a visit of a page by a query block
+// 7 ns; unpacking in place takes 8 to 16.
+bool unpack_first(const Kv4Shape &k) {
     if (k.n * k.max_pages * k.Hkv * kPairBytes > ((int64_t)2 << 30)) return false;
-    if (!k.lists) return s.pairs >= 3;
-    return (double)(k.Hq / k.Hkv) * (double)ceil_div(s.rows, kBlock) * (double)k.max_sel >
-           2.0 * (double)k.max_pages;
+    const int64_t blocks = shape_of(k, 1).per;  // query blocks of a stripe
+    if (!k.lists) return blocks > kInPlaceBlocks;
+    return (double)(k.Hq / k.Hkv) * (double)blocks * (double)k.max_sel >
+           (double)kInPlaceBlocks * (double)k.max_pages;
 }
 
 }  // namespace
 
-int64_t kv4_attn_many_rows(const Kv4Shape &k) {
-    return shape_of(k.n, k.Hq, k.Hkv, k.Lq, k.lists).rows;
-}
+int64_t kv4_attn_many_rows(const Kv4Shape &k) { return shape_of(k, 1).rows; }
 
 int64_t kv4_attn_many_work_bytes(const Kv4Shape &k) {
-    const Shape s = shape_of(k.n, k.Hq, k.Hkv, k.Lq, k.lists);
-    return kHeadBytes + part_bytes(s) +
-           (unpack_first(s, k) ? k.n * k.max_pages * k.Hkv * kPairBytes : 0);
+    const bool first = unpack_first(k);
+    return kHeadBytes + part_bytes(shape_of(k, first ? 2 : 1)) +
+           (first ? k.n * k.max_pages * k.Hkv * kPairBytes : 0);
 }
 
 cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape &k,
                                  cudaStream_t stream) {
-    const Shape s = shape_of(k.n, k.Hq, k.Hkv, k.Lq, k.lists);
+    const bool first = unpack_first(k);
+    const Shape s = shape_of(k, first ? 2 : 1);
     CUtensorMap mq;
     if (!encode(&mq, a.q, s.stripes, s.rows)) return cudaErrorUnknown;
     Plan p;
     p.heads = a.Hq / c.Hkv;
     p.rows = (int)s.rows;
-    p.pairs = (int)s.pairs;
+    p.blocks = (int)s.blocks;
+    p.per = (int)s.per;
     p.nqb = (int)ceil_div(s.rows, kBlock);
-    const bool first = unpack_first(s, k);
     const int64_t entries = k.lists ? a.max_sel : c.max_pages;  // of a unit, at most
-    p.halved = s.halved();
-    const bool chooses = first && !k.lists && !p.halved && (a.n > 1 || a.causal) &&
-                         a.n * s.pairs <= kChosenUnits;
-    // Unpacking in place makes a step over a shared page 2.8 us, over a page
-    // of each block 4.8 us.
-    const float step = first ? 1.0f : p.halved || k.lists ? 2.5f : 1.5f;
-    const Cut cut = cut_of(s.units(), p.halved ? ceil_div(entries, 2) : entries, step, chooses,
-                           p.halved);
+    const bool chooses =
+        first && !k.lists && (a.n > 1 || a.causal) && a.n * s.per <= kChosenUnits;
+    // A step over a page unpacked in place: one block, 1.2 us.
+    const Cut cut = cut_of(s.units(), entries, first ? 1.0f : kInPlaceStep, chooses);
     p.whole = cut.whole, p.splits = cut.splits;
     p.chunk = (int)ceil_div(entries > 0 ? entries : 1, p.splits);
     p.chosen = chooses && p.splits > 1
@@ -1114,18 +1108,19 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
     if (first) {
         unpack_kernel<<<(unsigned)((int64_t)a.n * c.max_pages * c.Hkv + (p.chosen ? 1 : 0)), 256,
                         0, stream>>>(c, a, p);
-        e = launch_after(kernel, grid, kThreads<true>, kSmemBytes, stream, mq, c, a, p);
+        e = cudaGetLastError();
+        if (e == cudaSuccess)
+            e = launch_after(kernel, grid, kThreads<true>, kSmemBytes, stream, mq, c, a, p);
     } else {
         kernel<<<grid, kThreads<false>, kSmemBytes, stream>>>(mq, c, a, p);
         e = cudaGetLastError();
     }
-    if (e != cudaSuccess || (!p.halved && p.splits == 1) || tail == 0) return e;
+    if (e != cudaSuccess || p.splits == 1 || tail == 0) return e;
     // Eight rows a CTA while these fit the GPU at once, then 32, which find
     // their unit once.
-    const int64_t rows = tail * (p.halved ? kBlock : kPartRows);
+    const int64_t rows = tail * p.blocks * kBlock;
     p.join_rows = rows / 8 <= 148 * 8 ? 8 : 32;
-    return launch_after(many_join_kernel, (unsigned)(rows / p.join_rows),
-                        256, 0, stream, c, a, p);
+    return launch_after(many_join_kernel, (unsigned)(rows / p.join_rows), 256, 0, stream, c, a, p);
 }
 
 }  // namespace sparstar
