@@ -6,7 +6,7 @@ namespace {
 
 // The tcgen05 kernel multiplies 128 rows whatever it is given, the other one
 // 8 or 16.
-constexpr int64_t kManyRows = 49;
+constexpr int64_t kManyRows = 33;
 
 bool many(const Kv4Shape &s, float tau) {
     // tau: the kernel takes the maximum of the scores before it scales them.

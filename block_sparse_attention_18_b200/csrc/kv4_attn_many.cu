@@ -15,16 +15,16 @@
 //     share a key head (the heads of a group lie one behind the other in q)
 //     and walk the same pages: a tile serves 256 rows.  With lists each block
 //     walks its own.
-//   unpacked in place: seven warps of the attention kernel read the packed
-//     pages into registers (the next tile's words and the page of the one
-//     after are on their way while this one is unpacked), dequantise them and
-//     write them to the ring.  Only the packed bytes cross HBM: right for few
-//     query blocks and long caches.  One query block a CTA, with two TMEM
-//     buffers for its scores; one warp issues both products, polling for
-//     whichever is ready.  Twelve warps keep 168 registers each (a row of
-//     scores stays in registers).  With three unpacking warps beside two
-//     blocks' softmax, unpacking was the bound: 2.4 us a page and block
-//     against 1.2 now.
+//   unpacked in place: the attention kernel brings the packed halves of the
+//     pages into a small ring by bulk copies; six warps dequantise them from
+//     there into the ring of tiles.  Only the packed bytes cross HBM: right for few
+//     query blocks and long caches.  One query block a CTA.  Its softmax has
+//     two threads a row, of 64 tokens of each tile, which never meet: each
+//     half has its own maximum, sum and accumulator (O of tokens 0-63 and of
+//     64-127 of every tile), joined at the end.  Two short chains a tile take
+//     half the time of one long one, and 64 scores fit beside the rest in the
+//     128 registers of sixteen warps.  One warp issues all products, polling
+//     for whichever is ready.
 //
 // Values lie channel by channel in a page, so both operands are K-major.  Few
 // CTAs (short stripes, long caches) split the pages among several; a kernel
@@ -38,42 +38,41 @@ namespace {
 // Query blocks a CTA.
 template <bool kPre>
 constexpr int kBlocks = kPre ? 2 : 1;
-// Unpacked first: warps 0-3 softmax of block A, 4-7 of B, 8 copies, 9 issues
-// S = Q K^T, 10 O += P V.  In place: 0-3 softmax, 4-10 unpack, 11 issues both.
+// Warps 0-7: softmax, of blocks A and B or of both halves of the tiles.
+// Unpacked first: 8 copies, 9 issues S = Q K^T, 10 O += P V.  In place: 8-13
+// unpack, 14 copies, 15 issues both products.
 template <bool kPre>
-constexpr int kThreads = kPre ? 352 : 384;
+constexpr int kThreads = kPre ? 352 : 512;
 template <bool kPre>
-constexpr int kLoadWarp = kPre ? 8 : 11;   // Q, barriers
+constexpr int kLoadWarp = kPre ? 8 : 14;   // Q, tiles or packed halves, barriers
 template <bool kPre>
-constexpr int kMmaWarp = kPre ? 9 : 11;    // TMEM, S = Q K^T
-constexpr int kPvWarp = 10, kUnpackWarp = 4, kUnpackWarps = 7;
+constexpr int kMmaWarp = kPre ? 9 : 15;    // TMEM, S = Q K^T
+constexpr int kPvWarp = 10, kUnpackWarp = 8, kUnpackWarps = 6;
 constexpr int kUnpackStrips = 3;  // of 16 strips of eight rows, a warp at most
 constexpr uint32_t kTmemCols = 512;
-// TMEM columns: scores of step j, P and O of block x.
-template <bool kPre>
-__device__ constexpr uint32_t col_s(int j) {
-    return kPre ? 0u : (j & 1) * 128u;
-}
+// TMEM columns: S; P and O of block (or half) x, P of a half 32 columns.
+constexpr uint32_t kColS = 0;
 template <bool kPre>
 __device__ constexpr uint32_t col_p(int x) {
-    return kPre ? (x ? 192u : 128u) : 256u;
+    return 128u + (kPre ? 64u : 32u) * x;
 }
-template <bool kPre>
-__device__ constexpr uint32_t col_o(int x) {
-    return kPre ? (x ? 384u : 256u) : 384u;
-}
+__device__ constexpr uint32_t col_o(int x) { return 256u + 128u * x; }
 
 constexpr int kOffQ = 0;
 constexpr int kOffStage = 2 * kTileBytes;
+// In place: packed halves of pages, where Q_B would be.
+constexpr int kOffPacked = kTileBytes, kPackedStages = 3;
+static_assert(kPackedStages * kv4_half_bytes(kHD) <= kTileBytes, "packed ring");
 constexpr int kOffBar = kOffStage + kStages * kTileBytes;
 struct Bars {
     uint64_t q_full;
     uint64_t st_full[kStages][2];  // [stage][use & 1], see ring_parity
     uint64_t st_empty[kStages];
-    uint64_t s_full[2];  // unpacked first: of block A, B; in place: of the two buffers
-    uint64_t s_free[2];  // unpacked first: [0]; in place: of the two buffers
-    uint64_t p_full[2][2];
-    uint64_t pv_done[2];
+    uint64_t packed_full[kPackedStages], packed_empty[kPackedStages];
+    uint64_t s_full[2];  // S of block A, B; in place: [0]
+    uint64_t s_free;
+    uint64_t p_full[2][2];  // [block][half of the tile]; in place: [0][half]
+    uint64_t pv_done[2];    // of a block, of a half
     uint64_t drain;
     uint32_t tmem_base;
     int32_t abort_flag;
@@ -416,7 +415,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
     };
     auto bar_empty = [&](int s) { return smem_addr(&bars->st_empty[s]); };
     auto bar_s = [&](int x) { return smem_addr(&bars->s_full[x]); };
-    auto bar_sfree = [&](int b) { return smem_addr(&bars->s_free[b]); };
+    const uint32_t bar_sfree = smem_addr(&bars->s_free);
     auto bar_p = [&](int x, int h) { return smem_addr(&bars->p_full[x][h]); };
     auto bar_pv = [&](int x) { return smem_addr(&bars->pv_done[x]); };
     const uint32_t bar_drain = smem_addr(&bars->drain);
@@ -429,9 +428,13 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 mbar_init(smem_addr(&bars->st_full[s][1]), kPre ? 1 : kUnpackWarps);
                 mbar_init(bar_empty(s), 1);
             }
+            for (int s = 0; s < kPackedStages; ++s) {
+                mbar_init(smem_addr(&bars->packed_full[s]), 1);
+                mbar_init(smem_addr(&bars->packed_empty[s]), kUnpackWarps);
+            }
+            mbar_init(bar_sfree, kPre ? kBlock : 2 * kBlock);  // the readers of one S
             for (int x = 0; x < 2; ++x) {
                 mbar_init(bar_s(x), 1);
-                mbar_init(bar_sfree(x), kBlock);
                 for (int h = 0; h < 2; ++h) mbar_init(bar_p(x, h), kBlock);
                 mbar_init(bar_pv(x), 1);
             }
@@ -501,6 +504,8 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         if (tile & 2) return wb.next(tile & 1 ? cur_v[1] : cur_k[1], page);
         return wa.next(tile & 1 ? cur_v[0] : cur_k[0], page);
     };
+    auto bar_packed = [&](int s) { return smem_addr(&bars->packed_full[s]); };
+    auto bar_unpacked = [&](int s) { return smem_addr(&bars->packed_empty[s]); };
     auto load_q = [&]() {  // by one lane
         const uint64_t pol = policy_evict_first();
         const int nq = nB > 0 ? 2 : 1;
@@ -526,30 +531,32 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
 #pragma unroll
             for (int kk = 0; kk < kHD / 16; ++kk) {
                 const uint64_t o = (uint64_t)(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4);
-                mma_ss(tmem + col_s<kPre>(j), dQ + o, dK + o, kIdesc, kk > 0 ? 1u : 0u);
+                mma_ss(tmem + kColS, dQ + o, dK + o, kIdesc, kk > 0 ? 1u : 0u);
             }
             if (frees) mma_commit(bar_empty(stage));
-            mma_commit(bar_s(kPre ? x : j & 1));
+            mma_commit(bar_s(x));
         }
         __syncwarp();
     };
-    // O_x += P_x V over tokens 64 h .. 64 h + 63 of ring slot e.
+    // O += P V over tokens 64 h .. 64 h + 63 of ring slot e: of block x, or of
+    // half h.
     auto issue_pv = [&](int x, int j, int h, int e) {
         const int stage = e % kStages;
         const uint64_t dV = desc_k_major(base + kOffStage + stage * kTileBytes);
         const bool frees = apart || x == 1 || j >= nB;
+        const uint32_t dO = tmem + col_o(kPre ? x : h);
+        const uint32_t aP = tmem + (kPre ? col_p<kPre>(x) + 32u * h : col_p<kPre>(h));
+        const bool fresh = j == 0 && (!kPre || h == 0);
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
             for (int kq = 0; kq < 4; ++kq) {
                 const uint64_t o = (uint64_t)((h * kPanelBytes + kq * 32) >> 4);
-                mma_ts(tmem + col_o<kPre>(x), tmem + col_p<kPre>(x) + 8u * (4 * h + kq), dV + o, kIdesc,
-                       h > 0 || kq > 0 || j > 0 ? 1u : 0u);
+                mma_ts(dO, aP + 8u * kq, dV + o, kIdesc, fresh && kq == 0 ? 0u : 1u);
             }
-            if (h == 1) {
-                if (frees) mma_commit(bar_empty(stage));
-                mma_commit(bar_pv(x));
-            }
+            if (h == 1 && frees) mma_commit(bar_empty(stage));
+            if (!kPre) mma_commit(bar_pv(h));
+            else if (h == 1) mma_commit(bar_pv(x));
         }
         __syncwarp();
     };
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 const int e = k_slot(x, j);
                 ok = wait_warp(bar_full(e), ring_parity(e), abort_flag, status) &&
                      (n == 0 ||
-                      wait_warp(bar_sfree(0), (uint32_t)(n - 1) & 1u, abort_flag, status));
+                      wait_warp(bar_sfree, (uint32_t)(n - 1) & 1u, abort_flag, status));
                 if (!ok) break;
                 issue_qk(x, j, e);
                 ++n;
@@ -626,10 +633,35 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             if (lane == 0) drain_wait(bar_drain, 0);
         }
         __syncwarp();
+    } else if (!kPre && warp == kLoadWarp<kPre>) {
+        // ------------------------------- copying warp: Q, packed halves
+        if (lane == 0 && nmax > 0) {
+            load_q();
+            constexpr int kHalf = kv4_half_bytes(kHD);
+            int e = 0, page;
+            for (int tile = next_tile(); tile >= 0; tile = next_tile()) {
+                find(tile, page);
+                const int s = e % kPackedStages;
+                if (!wait1(bar_unpacked(s), ((uint32_t)(e / kPackedStages) & 1u) ^ 1u,
+                           abort_flag, status))
+                    break;
+                mbar_expect_tx(bar_packed(s), kHalf);
+                const uint8_t *src =
+                    c.pages + ((int64_t)page * c.Hkv + kh) * (2 * kHalf) + (tile & 1) * kHalf;
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+                    "[%1], %2, [%3];" ::"r"(base + kOffPacked + s * kHalf),
+                    "l"(src), "r"(kHalf), "r"(bar_packed(s))
+                    : "memory");
+                ++e;
+            }
+            // Copies in flight land before the CTA may exit.
+            drain_wait(bar_q, 0);
+            for (int i = e > kPackedStages ? e - kPackedStages : 0; i < e; ++i)
+                drain_wait(bar_packed(i % kPackedStages), (uint32_t)(i / kPackedStages) & 1u);
+        }
     } else if (!kPre && warp == kMmaWarp<kPre>) {
         // ----------------------- both products, whichever is ready next
-        if (lane == 0 && nmax > 0) load_q();
-        __syncwarp();
         bool ok = nmax > 0 && wait_warp(bar_q, 0, abort_flag, status);
         auto ready = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_poll(bar, parity));
@@ -641,9 +673,8 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             bool moved = false;
             if (qj < nA) {
                 const int e = k_slot(0, qj);
-                // The buffer's scores before these have been read.
                 if (ready(bar_full(e), ring_parity(e)) &&
-                    (qj < 2 || ready(bar_sfree(qj & 1), (uint32_t)((qj >> 1) - 1) & 1u))) {
+                    (qj == 0 || ready(bar_sfree, (uint32_t)(qj - 1) & 1u))) {
                     issue_qk(0, qj, e);
                     ++qj;
                     moved = true;
@@ -676,105 +707,80 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         if (nmax > 0) {
             if (elect_one()) mma_commit(bar_drain);
             __syncwarp();
-            if (lane == 0) {
-                drain_wait(bar_drain, 0);
-                drain_wait(bar_q, 0);
-            }
+            if (lane == 0) drain_wait(bar_drain, 0);
         }
         __syncwarp();
     } else if (!kPre && warp >= kUnpackWarp) {
         // ------------------------------------------------- unpacking warps
-        // 16 strips of eight rows: 0-2, 3-5, then two each; in two groups of
-        // channels at most (a group is four strips).
+        // 16 strips of eight rows: three each, the last two warps two; in two
+        // groups of channels at most (a group is four strips).
         const int w = warp - kUnpackWarp, g = lane & 3, q = lane >> 2;
-        const int strip0 = w < 2 ? 3 * w : 2 * w + 2, strips = w < 2 ? 3 : 2;
+        const int strip0 = w < 5 ? 3 * w : 14, strips = w < 4 ? 3 : 2;
+        const int in_first = 4 - (strip0 & 3);  // strips of the first group
         const Unpack u(lane);
-        const int64_t head = (int64_t)kh * kv4_page_bytes(kHD);
-        const int64_t page_bytes = (int64_t)c.Hkv * kv4_page_bytes(kHD);
-        uint4 code[kUnpackStrips], vs[2][2];
-        uint32_t ks[kUnpackStrips];
-        auto load = [&](int tile, int page) {
-            const uint8_t *half = c.pages + page * page_bytes + head +
-                                  (tile & 1) * kv4_half_bytes(kHD);
+        constexpr int kHalf = kv4_half_bytes(kHD);
+        int e = 0;
+        for (int tile = next_tile(); tile >= 0; tile = next_tile(), ++e) {
+            const int s = e % kPackedStages, stage = e % kStages;
+            if (!wait_warp(bar_packed(s), (uint32_t)(e / kPackedStages) & 1u, abort_flag, status))
+                break;
+            const uint8_t *half = smem + kOffPacked + s * kHalf;
+            const uint8_t *scales = half + kv4_code_bytes(kHD);
+            uint4 code[kUnpackStrips];
 #pragma unroll
             for (int i = 0; i < kUnpackStrips; ++i)
                 if (i < strips)
-                    code[i] = __ldg(reinterpret_cast<const uint4 *>(half) +
-                                    ((strip0 + i) * 8 + q) * 4 + g);
-            const uint8_t *s = half + kv4_code_bytes(kHD);
-            if (tile & 1) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint4 *sv = reinterpret_cast<const uint4 *>(
-                        s + min((strip0 >> 2) + k, 3) * kBlock + 32 * g);
-                    vs[k][0] = __ldg(sv), vs[k][1] = __ldg(sv + 1);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kUnpackStrips; ++i)
-                    if (i < strips) ks[i] = __ldg(s + ((strip0 + i) * 8 + q) * 4 + g);
-            }
-        };
-        int e = 0, page = 0, page1 = 0, page2 = 0;
-        int tile = next_tile();
-        if (tile >= 0) {
-            find(tile, page);
-            load(tile, page);
-        }
-        int tile1 = next_tile();
-        if (tile1 >= 0) find(tile1, page1);
-        while (tile >= 0) {
-            uint4 now[kUnpackStrips], vn[2][2];
-            uint32_t kn[kUnpackStrips];
-#pragma unroll
-            for (int i = 0; i < kUnpackStrips; ++i) now[i] = code[i], kn[i] = ks[i];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) vn[k][0] = vs[k][0], vn[k][1] = vs[k][1];
-            const int tile2 = next_tile();
-            if (tile2 >= 0) find(tile2, page2);
-            if (tile1 >= 0) load(tile1, page1);
-            const int stage = e % kStages;
+                    code[i] =
+                        reinterpret_cast<const uint4 *>(half)[((strip0 + i) * 8 + q) * 4 + g];
             if (!wait_warp(bar_empty(stage), ((uint32_t)(e / kStages) & 1u) ^ 1u, abort_flag,
                            status))
                 break;
             const uint32_t dst = base + kOffStage + stage * kTileBytes;
             auto put = [&](uint32_t at, const uint4 &v) {
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + at),
-                             "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                             : "memory");
+                             "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
             };
             if (tile & 1) {
-                const int in_first = 4 - (strip0 & 3);  // strips of the first group
+                auto pairs_of = [&](int group, Unpack::Pairs &pairs) {
+                    const uint4 *sv =
+                        reinterpret_cast<const uint4 *>(scales + group * kBlock + 32 * g);
+                    u.pairs(sv[0], sv[1], pairs);
+                };
                 Unpack::Pairs pairs;
-                u.pairs(vn[0][0], vn[0][1], pairs);
+                pairs_of(strip0 >> 2, pairs);
 #pragma unroll
                 for (int i = 0; i < kUnpackStrips; ++i) {
-                    if (i == in_first) u.pairs(vn[1][0], vn[1][1], pairs);
-                    if (i < strips) u.values(now[i], pairs, strip0 + i, put);
+                    if (i >= strips) break;
+                    if (i == in_first) pairs_of((strip0 >> 2) + 1, pairs);
+                    u.values(code[i], pairs, strip0 + i, put);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < kUnpackStrips; ++i)
-                    if (i < strips) u.keys(now[i], kn[i], strip0 + i, put);
+                    if (i < strips)
+                        u.keys(code[i], scales[((strip0 + i) * 8 + q) * 4 + g], strip0 + i, put);
             }
             // The MMAs read through the async proxy.
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_full(e));
-            ++e;
-            tile = tile1, tile1 = tile2, page1 = page2;
+            if (lane == 0) {
+                mbar_arrive(bar_full(e));
+                mbar_arrive(bar_unpacked(s));
+            }
         }
     } else {
         // ------------------------------- softmax + epilogue (128 per block)
-        const int x = warp >> 2;
+        constexpr int kCols = kPre ? kBlock : kBlock / 2;  // tokens of a tile a thread has
+        const int x = warp >> 2;  // block, or half of the tiles
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const uint32_t colO = col_o<kPre>(x), colP = col_p<kPre>(x);
-        const int nx = x == 0 ? nA : nB;
+        const uint32_t colO = col_o(x), colP = col_p<kPre>(x);
+        const int col0 = kPre ? 0 : kCols * x;
+        const int nx = !kPre || x == 0 ? nA : nB;
         const float sc = p.sc;
         const Walk wx = !kPre || x == 0 ? walk[0] : walk[1];
-        const int grow = (qb0 + x) * kBlock + row;  // of the stripe
+        const int grow = (qb0 + (kPre ? x : 0)) * kBlock + row;  // of the stripe
         const bool real = grow < p.rows;
         // Tokens the row sees; a tile is masked where a row sees part of it.
         const int seen = a.causal ? L - a.Lq + 1 + grow % a.Lq : L;
@@ -786,41 +792,41 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             int kb, page;
             if (plain) kb = wx.list ? __ldg(wx.list + wx.lo + j) : wx.lo + j;
             else kb = wx.next(cur, page);
-            const int buffer = kPre ? x : j & 1;
-            if (!wait_warp(bar_s(buffer), (uint32_t)(kPre ? j : j >> 1) & 1u, abort_flag, status)) {
+            if (!wait_warp(bar_s(kPre ? x : 0), (uint32_t)j & 1u, abort_flag, status)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            float s[128];
+            float s[kCols];
             {
-                uint32_t r[4][32];
+                uint32_t r[kCols / 32][32];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(tmem + lane_base + col_s<kPre>(j) + 32 * q, r[q]);
+                for (int q = 0; q < kCols / 32; ++q)
+                    tmem_ld32(tmem + lane_base + kColS + col0 + 32 * q, r[q]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) reg_fence(r[q]);
+                for (int q = 0; q < kCols / 32; ++q) reg_fence(r[q]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < kCols / 32; ++q)
 #pragma unroll
                     for (int u = 0; u < 32; ++u) s[32 * q + u] = __uint_as_float(r[q][u]);
             }
             tc_fence_before();
-            mbar_arrive(bar_sfree(kPre ? 0 : buffer));
-            const int valid = seen - kb * kBlock;
-            if (__any_sync(0xffffffffu, valid < kBlock)) {
+            mbar_arrive(bar_sfree);
+            const int valid = seen - kb * kBlock - col0;
+            if (__any_sync(0xffffffffu, valid < kCols)) {
 #pragma unroll
-                for (int q = 0; q < kBlock; ++q)
+                for (int q = 0; q < kCols; ++q)
                     if (q >= valid) s[q] = -INFINITY;
             }
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int q = 4; q + 8 <= kBlock; q += 8) {
+            for (int q = 4; q + 8 <= kCols; q += 8) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) mx[t] = max3f(mx[t], s[q + t], s[q + 4 + t]);
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) mx[t] = fmaxf(mx[t], s[kBlock - 4 + t]);
+            for (int t = 0; t < 4; ++t) mx[t] = fmaxf(mx[t], s[kCols - 4 + t]);
             const float m_tile = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * sc;
             const float m_new = fmaxf(m_ref, m_tile);
             bool pv_seen = false;
@@ -828,7 +834,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 if (j > 0) {
                     if (!wait_warp(bar_pv(x), (uint32_t)(j - 1) & 1u, abort_flag, status)) {
                         ok = false;
-                break;
+                        break;
                     }
                     tc_fence_after();
                     pv_seen = true;
@@ -856,15 +862,15 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             if (j > 0 && !pv_seen) {
                 if (!wait_warp(bar_pv(x), (uint32_t)(j - 1) & 1u, abort_flag, status)) {
                     ok = false;
-                break;
+                    break;
                 }
                 tc_fence_after();
             }
             const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(neg_m, neg_m);
             float ls[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t pk[64];
+            uint32_t pk[kCols / 2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < kCols / 64; ++h) {
 #pragma unroll
                 for (int u = 32 * h; u < 32 * h + 32; u += 2) {
                     const int q = 2 * u;
@@ -882,56 +888,106 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 tmem_st32(tmem + lane_base + colP + 32 * h, pk + 32 * h);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar_p(x, h));
+                mbar_arrive(kPre ? bar_p(x, h) : bar_p(0, x));
             }
             l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
         }
 
         // ---- epilogue
-        const bool have = nx > 0 && ok &&
-                          wait_warp(bar_pv(x), (uint32_t)(nx - 1) & 1u, abort_flag, status);
+        bool have = nx > 0 && ok &&
+                    wait_warp(bar_pv(x), (uint32_t)(nx - 1) & 1u, abort_flag, status);
         if (have) tc_fence_after();
+        float fa = 1.0f, fb = 0.0f;  // weights of this half and the other
+        float *other = reinterpret_cast<float *>(smem + kOffStage) + row * (kHD + 4);
+        if constexpr (!kPre) {
+            // The second half's results pass through the ring, which nobody
+            // reads any more, to the first half's threads.
+            float *rest = reinterpret_cast<float *>(smem + kOffStage) + kBlock * (kHD + 4);
+            if (x == 1) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t r[32];
+                    if (have) {
+                        tmem_ld32(tmem + lane_base + colO + 32 * q, r);
+                        tmem_wait_ld();
+                        reg_fence(r);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            reinterpret_cast<uint4 *>(other + 32 * q)[u] =
+                                make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+                    }
+                }
+                rest[row] = m_ref, rest[kBlock + row] = l;
+                rest[2 * kBlock + row] = have ? 1.0f : 0.0f;
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(2 * kBlock) : "memory");
+            if (x == 0 && have) {
+                const float mb = rest[row], lb = rest[kBlock + row];
+                have = rest[2 * kBlock + row] != 0.0f;
+                const float top = fmaxf(m_ref, mb);
+                fa = m_ref > -INFINITY ? ex2(m_ref - top) : 0.0f;
+                fb = mb > -INFINITY ? ex2(mb - top) : 0.0f;
+                l = l * fa + lb * fb;
+                m_ref = top;
+            }
+            have = __all_sync(0xffffffffu, have);
+        }
         const int64_t out_row = (int64_t)stripe * p.rows + grow;
-        float *part = p.parts + (int64_t)(joins ? tail * kBlocks<kPre> + x : 0) * kPartFloats;
+        float *part = p.parts + (int64_t)(joins ? tail * kBlocks<kPre> + (kPre ? x : 0) : 0) *
+                                    kPartFloats;
         float *part_o = part + 2 * kBlock + (int64_t)row * kHD;
         // A row without a weight (no token seen) gets 0.
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if (kPre || x == 0) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t r[32];
+            for (int q = 0; q < 4; ++q) {
+                uint32_t r[32];
 #pragma unroll
-            for (int u = 0; u < 32; ++u) r[u] = 0;
-            if (have) {
-                tmem_ld32(tmem + lane_base + colO + 32 * q, r);
-                tmem_wait_ld();
-                reg_fence(r);
-            }
-            if (!real || (nx > 0 && !have)) continue;
-            if (joins) {
+                for (int u = 0; u < 32; ++u) r[u] = 0;
+                if (have) {
+                    tmem_ld32(tmem + lane_base + colO + 32 * q, r);
+                    tmem_wait_ld();
+                    reg_fence(r);
+                    if constexpr (!kPre) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    reinterpret_cast<uint4 *>(part_o + 32 * q)[u] =
-                        make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
-            } else {
-                uint4 *o4 = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                      out_row * kHD + 32 * q);
+                        for (int u = 0; u < 8; ++u) {
+                            const float4 b = reinterpret_cast<const float4 *>(other + 32 * q)[u];
+                            const float v[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    uint32_t v[4];
+                            for (int k = 0; k < 4; ++k)
+                                r[4 * u + k] = __float_as_uint(
+                                    fmaf(fb, v[k], fa * __uint_as_float(r[4 * u + k])));
+                        }
+                    }
+                }
+                if (!real || (nx > 0 && !have)) continue;
+                if (joins) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] = nx == 0 ? 0u
+                    for (int u = 0; u < 8; ++u)
+                        reinterpret_cast<uint4 *>(part_o + 32 * q)[u] =
+                            make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+                } else {
+                    uint4 *o4 = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                          out_row * kHD + 32 * q);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = nx == 0
+                                       ? 0u
                                        : pack_bf16(__uint_as_float(r[8 * u + 2 * k]) * inv,
                                                    __uint_as_float(r[8 * u + 2 * k + 1]) * inv);
-                    __stcs(o4 + u, make_uint4(v[0], v[1], v[2], v[3]));
+                        __stcs(o4 + u, make_uint4(v[0], v[1], v[2], v[3]));
+                    }
                 }
             }
-        }
-        if (joins) {
-            part[row] = m_ref;
-            part[kBlock + row] = l;
-        } else if (real && a.lse && (nx == 0 || have)) {
-            a.lse[out_row] = (m_ref + log2f(l)) * 0.6931471805599453f;
+            if (joins) {
+                part[row] = m_ref;
+                part[kBlock + row] = l;
+            } else if (real && a.lse && (nx == 0 || have)) {
+                a.lse[out_row] = (m_ref + log2f(l)) * 0.6931471805599453f;
+            }
         }
     }
 
@@ -1022,7 +1078,7 @@ Shape shape_of(const Kv4Shape &k, int64_t blocks) {
 // How a call's units are cut.  Where the device chooses the chunk: as many
 // CTAs a unit as the scratch holds.  Else, for units of equal length: whole
 // units in full waves first, the others split, as cheap as that gets.
-constexpr float kInPlaceStep = 0.7f;
+constexpr float kInPlaceStep = 0.85f;
 constexpr int kInPlaceBlocks = 4;
 struct Cut {
     int whole, splits;
