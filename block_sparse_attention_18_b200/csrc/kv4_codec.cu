@@ -83,7 +83,9 @@ struct GroupBf16 {
                                            __float_as_uint(fmaf(b, up, kRound + 8.0f)), 0x5410);
             const uint32_t d = __byte_perm(__float_as_uint(fmaf(a, down, kRound + 8.0f)),
                                            __float_as_uint(fmaf(b, down, kRound + 8.0f)), 0x5410);
-            p[k] = __vmaxu2(u, d) & ~((u ^ d) & 0x00010001u);
+            uint32_t m;
+            asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(u), "r"(d));
+            p[k] = m & ~((u ^ d) & 0x00010001u);
         }
         return join_pairs(p);
     }
@@ -273,7 +275,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, uint32_t w, uint32_t co
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = kv4_dequant(kv4_pair128(w, i, kMagic), s, m);
-    *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(o[0], o[1], o[2], o[3]));
 }
 __device__ __forceinline__ void store8(float *p, uint32_t w, uint32_t code) {
     const float s = kv4_scale(code);
@@ -281,8 +283,8 @@ __device__ __forceinline__ void store8(float *p, uint32_t w, uint32_t code) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         o[e] = s * (float)((int)((w >> (4 * kv4_nibble(e))) & 15u) - 8);
-    reinterpret_cast<float4 *>(p)[0] = make_float4(o[0], o[1], o[2], o[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(o[4], o[5], o[6], o[7]);
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(o[0], o[1], o[2], o[3]));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(o[4], o[5], o[6], o[7]));
 }
 
 template <typename T, int D>
@@ -299,33 +301,71 @@ __global__ void __launch_bounds__(kThreads)
     const uint8_t *half_v = half_k + kv4_half_bytes(D);
     const int64_t row = ((int64_t)sp.i * c.Hkv + sp.h) * tokens;
     const int first = sp.t0 - sp.shift, last = sp.t1 - sp.shift;
+    // The values' words first: they are on their way while the keys pass.
+    const int w0 = first / 8, tiles = W * ((last + 7) / 8 - w0);  // at most a thread's two
+    constexpr int kTiles = (W * (kBlock / 8) + kThreads - 1) / kThreads;
+    uint32_t r[kTiles][8];
+    auto tile_of = [&](int i, int &cw, int &tw) {
+        const int it = threadIdx.x + i * kThreads, n = (last + 7) / 8 - w0;
+        cw = it / n, tw = w0 + it % n;
+        return it < tiles;
+    };
+    if (v) {
+        const uint32_t *codes = reinterpret_cast<const uint32_t *>(half_v);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+            int cw, tw;
+            if (!tile_of(i, cw, tw)) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[i][e] = __ldg(codes + (cw * 8 + e) * (kBlock / 8) + tw);
+        }
+    }
+    const int items = (last - first) * W;
     if (k) {
         const uint32_t *codes = reinterpret_cast<const uint32_t *>(half_k);
         const uint8_t *scales = half_k + kv4_code_bytes(D);
-        for (int it = threadIdx.x; it < (last - first) * W; it += kThreads) {
-            const int slot = first + it / W, w = it % W;
-            store8(k + (row + slot + sp.shift) * D + w * 8, __ldg(codes + slot * W + w),
-                   __ldg(scales + slot * G + w / 4));
+        for (int it0 = threadIdx.x; it0 < items; it0 += 4 * kThreads) {
+            uint32_t word[4], scale[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int it = it0 + i * kThreads, slot = first + it / W, w = it % W;
+                if (it >= items) continue;
+                word[i] = __ldg(codes + slot * W + w);
+                scale[i] = __ldg(scales + slot * G + w / 4);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int it = it0 + i * kThreads, slot = first + it / W, w = it % W;
+                if (it < items)
+                    store8(k + (row + slot + sp.shift) * D + w * 8, word[i], scale[i]);
+            }
         }
     }
     if (v) {
-        const int w0 = first / 8, w1 = (last + 7) / 8;
-        const uint32_t *codes = reinterpret_cast<const uint32_t *>(half_v);
         const uint8_t *scales = half_v + kv4_code_bytes(D);
-        for (int it = threadIdx.x; it < W * (w1 - w0); it += kThreads) {
-            const int cw = it / (w1 - w0), tw = w0 + it % (w1 - w0);
-            uint32_t r[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = __ldg(codes + (cw * 8 + e) * (kBlock / 8) + tw);
-            kv4_transpose(r);
+        for (int i = 0; i < kTiles; ++i) {
+            int cw, tw;
+            if (!tile_of(i, cw, tw)) continue;
+            kv4_transpose(r[i]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) words[(tw * 8 + e) * kStride + cw] = r[e];
+            for (int e = 0; e < 8; ++e) words[(tw * 8 + e) * kStride + cw] = r[i][e];
         }
         __syncthreads();
-        for (int it = threadIdx.x; it < (last - first) * W; it += kThreads) {
-            const int slot = first + it / W, w = it % W;
-            store8(v + (row + slot + sp.shift) * D + w * 8, words[slot * kStride + w],
-                   __ldg(scales + (w / 4) * kBlock + slot));
+        for (int it0 = threadIdx.x; it0 < items; it0 += 4 * kThreads) {
+            uint32_t scale[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int it = it0 + i * kThreads, slot = first + it / W, w = it % W;
+                if (it < items) scale[i] = __ldg(scales + (w / 4) * kBlock + slot);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int it = it0 + i * kThreads, slot = first + it / W, w = it % W;
+                if (it < items)
+                    store8(v + (row + slot + sp.shift) * D + w * 8, words[slot * kStride + w],
+                           scale[i]);
+            }
         }
     }
 }
