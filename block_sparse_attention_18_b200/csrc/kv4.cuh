@@ -127,11 +127,18 @@ __device__ __forceinline__ int kv4_len(const Kv4 &c, int slot) {
     return L < 0 ? 0 : (L > most ? most : L);
 }
 
-// Launches a kernel that the one before it lets start early
-// (griddepcontrol.launch_dependents); it waits for that one's end itself.
+// A cache call's kernels follow each other closely (a step resizes, writes and
+// attends), so each may be launched while the one before it still runs: its
+// CTAs take their places as that one's leave, and each waits for the whole
+// grid before it, and for that one's own wait, before it touches memory.
+__device__ __forceinline__ void kv4_begin() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Launches such a kernel.
 template <typename... Args>
 inline cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned block, size_t smem,
-                         cudaStream_t stream, Args... args) {
+                                cudaStream_t stream, Args... args) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;

@@ -203,11 +203,27 @@ __device__ int64_t build_line(const Kv4 &c, const Kv4Attn &a, Line &line, int64_
     }
     if (lane == 31) sums[warp] = y;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) y += sums[w];
+#pragma unroll
+    for (int w = 0; w < kChunks / 32; ++w)
+        if (w < warp) y += sums[w];
     if (threadIdx.x < kChunks) shared[threadIdx.x + 1] = y;
     if (threadIdx.x == 0) shared[0] = 0;
     __syncthreads();
     return shared[kChunks];
+}
+
+__device__ __forceinline__ int64_t per_unit(int64_t x, int units) {
+    return x < 0x7fffffff ? (uint32_t)x / (uint32_t)units : x / units;
+}
+// The chunk of sequences that tile x lies in; for a whole warp.
+__device__ __forceinline__ int chunk_of(const Line &line, int64_t x, int units) {
+    static_assert(kChunks == 8 * 32, "two steps of a warp");
+    const int lane = threadIdx.x & 31;
+    const int64_t y = per_unit(x, units);
+    const uint32_t far = __ballot_sync(0xffffffffu, line.prefix[8 * lane] <= y);
+    const int lo = 8 * (31 - __clz(far));
+    const uint32_t near = __ballot_sync(0xffffffffu, line.prefix[lo + (lane & 7)] <= y);
+    return lo + 31 - __clz(near & 0xffu);
 }
 
 // One tile of the line.
@@ -216,16 +232,12 @@ struct Tile {
     int uid, block;
     int edge;        // 1: first tile of its unit, 2: last
 };
+// Tile x, looked up from a chunk `lo` that is not behind its own.
 template <int R>
 __device__ Tile locate(const Kv4 &c, const Kv4Attn &a, const Plan &p, const Line &line,
-                       int64_t x) {
-    const int64_t y = x < 0x7fffffff ? (uint32_t)x / (uint32_t)p.units : x / p.units;
-    int lo = 0, hi = kChunks;  // prefix[lo] <= y < prefix[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (line.prefix[mid] <= y) lo = mid;
-        else hi = mid;
-    }
+                       int64_t x, int lo) {
+    const int64_t y = per_unit(x, p.units);
+    while (line.prefix[lo + 1] <= y) ++lo;
     int64_t base = line.prefix[lo];
     int i = lo * line.chunk, L, T;
     while (base + (T = tiles_of(c, a, i, L)) <= y) base += T, ++i;
@@ -362,7 +374,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     // unit inside part k (2 k), what the part's end leaves (2 k + 1).
     __shared__ int32_t entry[2 * kParts], edges[2 * kParts];
     // Units with partial results: which entries, first row, rows; flags as edges.
-    __shared__ int32_t group_uid[2 * kParts], group_flags[2 * kParts], group_rows[2 * kParts];
+    __shared__ int32_t group_flags[2 * kParts], group_rows[2 * kParts];
     __shared__ uint32_t group_entries[2 * kParts];
     __shared__ int64_t group_row[2 * kParts];
     __shared__ int32_t cross[2], span[2][2], n_cross, n_groups;
@@ -379,6 +391,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         mbar_init(&taken[part], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    kv4_begin();
     Line line;
     const int64_t total = build_line(c, a, line, prefix, sums) * p.units;
     // Tiles a CTA; CTA k has the tiles from k * share.
@@ -415,7 +428,9 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         Tile t;
         t.src = t.uid = -1;
         t.block = t.edge = 0;
-        if (at + lane < x1) t = locate<R>(c, a, p, line, start + at + lane);
+        if (at >= x1) return t;
+        const int lo = chunk_of(line, start + at, p.units);
+        if (at + lane < x1) t = locate<R>(c, a, p, line, start + at + lane, lo);
         return t;
     };
     auto with_page = [&](const Tile &t) { return __ballot_sync(0xffffffffu, t.src >= 0); };
@@ -857,6 +872,39 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     // What each warp's registers hold, then the ends inside parts: [kHeld].
     float *so = reinterpret_cast<float *>(smem);  // [kHeld][R][kRow]
     float *sm = so + kHeld * R * kRow, *sl = sm + kHeld * R;
+    if (threadIdx.x >= kThreads - 32) {  // the last warp, often idle: an entry a lane
+        static_assert(2 * kParts <= 32, "an entry a lane");
+        const int id = lane < 2 * kParts ? entry[lane] : -1;
+        const int edge = id >= 0 ? edges[lane] : 0;
+        const uint32_t same = __match_any_sync(0xffffffffu, id);
+        const uint32_t below = (1u << lane) - 1;
+        const bool first = id >= 0 && (same & below) == 0;
+        const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+        const uint32_t enders = __ballot_sync(0xffffffffu, (edge & 2) != 0);
+        const int flags = (edge & 1) | ((enders & same) ? 2 : 0);
+        // At most two go on in other CTAs: the first and the last.
+        const uint32_t crossing = __ballot_sync(0xffffffffu, first && flags != 3);
+        if (lane == 0) n_groups = __popc(firsts), n_cross = __popc(crossing);
+        if (first) {
+            const int g = __popc(firsts & below);
+            const Unit un = unit_of<R>(c, a, p, id);
+            group_entries[g] = same;
+            group_flags[g] = flags;
+            group_row[g] = un.row;
+            group_rows[g] = un.rows;
+        }
+        if (first && flags != 3) {  // its CTAs
+            const int k = __popc(crossing & below), i = id / p.units;
+            int64_t at = line.prefix[i / line.chunk];
+            int L;
+            for (int s = i / line.chunk * line.chunk; s < i; ++s) at += tiles_of(c, a, s, L);
+            const int tiles = tiles_of(c, a, i, L);
+            at = at * p.units + (int64_t)(id - i * p.units) * tiles;
+            cross[k] = id;
+            span[k][0] = (int)(at / share);
+            span[k][1] = (int)((at + tiles - 1) / share);
+        }
+    }
     if (entry[2 * part + 1] >= 0) {
         const int w = part * kPair + member;
 #pragma unroll
@@ -886,30 +934,6 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
             sm[w * R + lane] = rec[R * D + lane];
             sl[w * R + lane] = rec[R * D + R + lane];
         }
-    }
-    if (threadIdx.x == 0) {
-        // Entries of one unit lie side by side, empty ones between them.
-        int n = 0, id = -1;
-        for (int en = 0; en < 2 * kParts; ++en) {
-            if (entry[en] < 0) continue;
-            if (entry[en] != id) {
-                id = group_uid[n] = entry[en];
-                group_entries[n] = 0;
-                group_flags[n++] = edges[en] & 1;
-            }
-            group_entries[n - 1] |= 1u << en;
-            group_flags[n - 1] |= edges[en] & 2;
-        }
-        n_groups = n;
-        n_cross = 0;
-    }
-    __syncthreads();
-    for (int g = threadIdx.x; g < n_groups; g += kThreads) {
-        const Unit un = unit_of<R>(c, a, p, group_uid[g]);
-        group_row[g] = un.row;
-        group_rows[g] = un.rows;
-        // At most two go on in other CTAs: the first and the last.
-        if (group_flags[g] != 3) cross[atomicAdd(&n_cross, 1)] = group_uid[g];
     }
     __syncthreads();
     for (int it = threadIdx.x; it < n_groups * (R * D / 4); it += kThreads) {
@@ -943,19 +967,12 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     // ---------------- units of several CTAs: the last one to arrive joins them
     __syncthreads();
     if (threadIdx.x < n_cross) {
-        const int id = cross[threadIdx.x], i = id / p.units;
-        int64_t first = line.prefix[i / line.chunk];
-        int L;
-        for (int s = i / line.chunk * line.chunk; s < i; ++s) first += tiles_of(c, a, s, L);
-        const int tiles = tiles_of(c, a, i, L);
-        first = first * p.units + (int64_t)(id - i * p.units) * tiles;
-        const int from = (int)(first / share), to = (int)((first + tiles - 1) / share);
+        const int from = span[threadIdx.x][0], to = span[threadIdx.x][1];
         __threadfence();
         const bool last = atomicAdd(p.arrived + from, 1u) == (uint32_t)(to - from);
         if (last) p.arrived[from] = 0;
         __threadfence();
-        span[threadIdx.x][0] = last ? from : -1;
-        span[threadIdx.x][1] = to;
+        if (!last) span[threadIdx.x][0] = -1;
     }
     __syncthreads();
     for (int k = 0; k < n_cross; ++k) {
@@ -977,8 +994,7 @@ cudaError_t launch(const Kv4 &c, const Kv4Attn &a, const Plan &p, cudaStream_t s
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
-    kernel<<<kCtas, 32 * kParts * kPair, kBytes, stream>>>(c, a, p);
-    return cudaGetLastError();
+    return launch_after(kernel, kCtas, 32 * kParts * kPair, kBytes, stream, c, a, p);
 }
 
 int stripe_rows(int64_t Hq, int64_t Hkv, int64_t Lq, bool lists) {

@@ -329,7 +329,7 @@ struct Unpack {
 // Unpacked first: one CTA a page and head of every sequence; four warps the
 // keys, four the values, 32 rows each.
 __global__ void __launch_bounds__(256) unpack_kernel(Kv4 c, Kv4Attn a, Plan p) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    kv4_begin();
     if (p.chosen && blockIdx.x == gridDim.x - 1) {  // one CTA behind the pages'
         choose_chunk(c, a, p);
         return;
@@ -381,8 +381,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
     // This CTA's pair of query blocks and part of their pages.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (kPre) asm volatile("griddepcontrol.wait;" ::: "memory");
+    kv4_begin();
     const int tail = (int)blockIdx.x - p.whole;  // CTA of the split units
     const int split = tail < 0 ? 0 : tail % p.splits;
     const Unit un = unit_of(c, a, p, tail < 0 ? blockIdx.x : p.whole + tail / p.splits);
@@ -1007,7 +1006,7 @@ __global__ void __launch_bounds__(256) many_join_kernel(Kv4 c, Kv4Attn a, Plan p
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.blocks * kBlock;  // of a unit
     const int at = blockIdx.x / (rows / p.join_rows);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    kv4_begin();
     const Unit u = unit_of(c, a, p, p.whole + at);
     if (u.parts == 1) return;
     const int n = u.parts;  // <= kMaxSplits
@@ -1162,15 +1161,13 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
     const int64_t tail = s.units() - p.whole;
     const unsigned grid = (unsigned)(p.whole + tail * p.splits);
     if (first) {
-        unpack_kernel<<<(unsigned)((int64_t)a.n * c.max_pages * c.Hkv + (p.chosen ? 1 : 0)), 256,
-                        0, stream>>>(c, a, p);
-        e = cudaGetLastError();
-        if (e == cudaSuccess)
-            e = launch_after(kernel, grid, kThreads<true>, kSmemBytes, stream, mq, c, a, p);
-    } else {
-        kernel<<<grid, kThreads<false>, kSmemBytes, stream>>>(mq, c, a, p);
-        e = cudaGetLastError();
+        const int64_t tiles = (int64_t)a.n * c.max_pages * c.Hkv;
+        e = launch_after(unpack_kernel, (unsigned)(tiles + (p.chosen ? 1 : 0)), 256, 0, stream, c,
+                         a, p);
+        if (e != cudaSuccess) return e;
     }
+    e = launch_after(kernel, grid, first ? kThreads<true> : kThreads<false>, kSmemBytes, stream,
+                     mq, c, a, p);
     if (e != cudaSuccess || p.splits == 1 || tail == 0) return e;
     // Eight rows a CTA while these fit the GPU at once, then 32, which find
     // their unit once.

@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads)
     constexpr int kStride = W + 1;    // odd: the transpose reads a column of words
     __shared__ uint32_t words[kBlock * kStride];  // value codes, token by token
     __shared__ uint8_t scales[G][kBlock];
+    kv4_begin();
     Span sp;
     if (!find_span(c, n, tokens, per_seq, seqs, starts, counts, true, status, sp)) return;
     uint8_t *half_k = c.pages + ((int64_t)sp.page * c.Hkv + sp.h) * kv4_page_bytes(D);
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(kThreads)
     constexpr int G = D / kGroup, W = D / 8;
     constexpr int kStride = W + 1;
     __shared__ uint32_t words[kBlock * kStride];
+    kv4_begin();
     Span sp;
     if (!find_span(c, n, tokens, per_seq, seqs, starts, counts, false, status, sp)) return;
     const uint8_t *half_k = c.pages + ((int64_t)sp.page * c.Hkv + sp.h) * kv4_page_bytes(D);
@@ -382,18 +384,14 @@ cudaError_t launch_kv4_write(const Kv4 &c, const void *k, const void *v, int dty
     const unsigned grid = (unsigned)((int64_t)n * per_seq * c.Hkv);
     auto go = [&](auto kernel, auto type) {
         using E = decltype(type);
-        kernel<<<grid, kThreads, 0, stream>>>(c, static_cast<const E *>(k),
-                                              static_cast<const E *>(v), n, T, per_seq, seqs,
-                                              starts, counts, status);
+        return launch_after(kernel, grid, kThreads, 0, stream, c, static_cast<const E *>(k),
+                            static_cast<const E *>(v), n, T, per_seq, seqs, starts, counts,
+                            status);
     };
-    if (dtype == SPARSTAR_BF16) {
-        if (c.D == 128) go(write_kernel<__nv_bfloat16, 128>, __nv_bfloat16());
-        else go(write_kernel<__nv_bfloat16, 64>, __nv_bfloat16());
-    } else {
-        if (c.D == 128) go(write_kernel<float, 128>, float());
-        else go(write_kernel<float, 64>, float());
-    }
-    return cudaGetLastError();
+    if (dtype == SPARSTAR_BF16)
+        return c.D == 128 ? go(write_kernel<__nv_bfloat16, 128>, __nv_bfloat16())
+                          : go(write_kernel<__nv_bfloat16, 64>, __nv_bfloat16());
+    return c.D == 128 ? go(write_kernel<float, 128>, float()) : go(write_kernel<float, 64>, float());
 }
 
 cudaError_t launch_kv4_read(const Kv4 &c, void *k, void *v, int dtype, int n, int64_t T,
@@ -403,17 +401,13 @@ cudaError_t launch_kv4_read(const Kv4 &c, void *k, void *v, int dtype, int n, in
     const unsigned grid = (unsigned)((int64_t)n * per_seq * c.Hkv);
     auto go = [&](auto kernel, auto type) {
         using E = decltype(type);
-        kernel<<<grid, kThreads, 0, stream>>>(c, static_cast<E *>(k), static_cast<E *>(v), n, T,
-                                              per_seq, seqs, starts, counts, status);
+        return launch_after(kernel, grid, kThreads, 0, stream, c, static_cast<E *>(k),
+                            static_cast<E *>(v), n, T, per_seq, seqs, starts, counts, status);
     };
-    if (dtype == SPARSTAR_BF16) {
-        if (c.D == 128) go(read_kernel<__nv_bfloat16, 128>, __nv_bfloat16());
-        else go(read_kernel<__nv_bfloat16, 64>, __nv_bfloat16());
-    } else {
-        if (c.D == 128) go(read_kernel<float, 128>, float());
-        else go(read_kernel<float, 64>, float());
-    }
-    return cudaGetLastError();
+    if (dtype == SPARSTAR_BF16)
+        return c.D == 128 ? go(read_kernel<__nv_bfloat16, 128>, __nv_bfloat16())
+                          : go(read_kernel<__nv_bfloat16, 64>, __nv_bfloat16());
+    return c.D == 128 ? go(read_kernel<float, 128>, float()) : go(read_kernel<float, 64>, float());
 }
 
 }  // namespace sparstar

@@ -285,13 +285,13 @@ __device__ void plan(const Kv4 &c, const int32_t *slots, const int32_t *src, con
 __global__ void __launch_bounds__(kPlanThreads)
     plan_kernel(Kv4 c, const int32_t *slots, const int32_t *src, const int32_t *lens, int n,
                 int32_t *status) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    kv4_begin();
     plan(c, slots, src, lens, n, status);
 }
 
 // Copies a short list: 16 bytes a thread.
 __global__ void __launch_bounds__(256) copy_few_kernel(Kv4 c) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    kv4_begin();
     const Work w = work_of(c);
     const int pairs = w.pairs[0];
     const int vecs = c.Hkv * (kv4_page_bytes(c.D) / 16);  // of a page
@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(256) copy_few_kernel(Kv4 c) {
 __global__ void __launch_bounds__(256)
     fork_shared_kernel(Kv4 c, const int32_t *src, const int32_t *dst, const int32_t *len, int n,
                        int32_t *status) {
+    kv4_begin();
     const int i = blockIdx.x;
     const int s = kv4_slot(c, src, i), d = kv4_slot(c, dst, i);
     bool bad = s < 0 || d < 0;
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(256)
 
 // Which pages move where, the counts after it.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Kv4 c, int32_t *n_live) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    kv4_begin();
     __shared__ int32_t sums[kWarps];
     const Work w = work_of(c);
     int live = 0, total;
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     copy_kernel(Kv4 c, bool remap, int32_t *status) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[kMaxStages];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    kv4_begin();
     const Work w = work_of(c);
     const int pairs = w.pairs[0];
     if (pairs == 0) return;
@@ -414,8 +415,8 @@ int64_t kv4_work_ints(int64_t n_pages, int64_t n_seqs) {
 
 cudaError_t launch_kv4_resize(const Kv4 &c, const int32_t *seqs, const int32_t *new_lens, int n,
                               int32_t *status, cudaStream_t stream) {
-    plan_kernel<<<1, kPlanThreads, 0, stream>>>(c, seqs, nullptr, new_lens, n, status);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(plan_kernel, 1, kPlanThreads, 0, stream, c, seqs,
+                                       static_cast<const int32_t *>(nullptr), new_lens, n, status);
     if (e != cudaSuccess) return e;
     return launch_after(copy_few_kernel, 148 * 4, 256, 0, stream, c);
 }
@@ -423,20 +424,18 @@ cudaError_t launch_kv4_resize(const Kv4 &c, const int32_t *seqs, const int32_t *
 cudaError_t launch_kv4_fork(const Kv4 &c, const int32_t *src, const int32_t *dst,
                             const int32_t *len, int n, bool deep, int32_t *status,
                             cudaStream_t stream) {
-    if (deep) {
-        plan_kernel<<<1, kPlanThreads, 0, stream>>>(c, dst, src, len, n, status);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        return launch_copy(c, false, status, stream);
-    } else {
-        fork_shared_kernel<<<n, 256, 0, stream>>>(c, src, dst, len, n, status);
-    }
-    return cudaGetLastError();
+    if (!deep)
+        return launch_after(fork_shared_kernel, (unsigned)n, 256, 0, stream, c, src, dst, len, n,
+                            status);
+    const cudaError_t e =
+        launch_after(plan_kernel, 1, kPlanThreads, 0, stream, c, dst, src, len, n, status);
+    if (e != cudaSuccess) return e;
+    return launch_copy(c, false, status, stream);
 }
 
 cudaError_t launch_kv4_compact(const Kv4 &c, int32_t *n_live, cudaStream_t stream) {
-    compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(c, n_live);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_after(compact_plan_kernel, 1, kPlanThreads, 0, stream, c, n_live);
     if (e != cudaSuccess) return e;
     return launch_copy(c, true, nullptr, stream);
 }

@@ -462,7 +462,7 @@ class Kv4Cache:
         self.Hkv, self.D, self.device = pages.shape[1], D, pages.device
         self.index = pages.get_device()
         self._work_of = {}  # stream handle -> scratch of its attention calls
-        self._need = {}     # sizes of an attention call -> bytes of its scratch
+        self._need = {}     # sizes of an attention call -> bytes of its scratch, a like of its lse
         self._struct = _Kv4Struct(pages.data_ptr(), refs.data_ptr(), table.data_ptr(),
                                   lens.data_ptr(), work.data_ptr(), n_pages, n_seqs,
                                   table.shape[1], pages.shape[1], D)
@@ -674,6 +674,8 @@ def sparstar_kv4_attn(cache: Kv4Cache, q, seqs=None, tau: float = None, causal: 
                                                 max_sel)
         if need < 0:
             raise SparstarError(EDTYPE if dt < 0 else EINVAL, "sparstar_kv4_attn")
+        # Making a tensor like another one costs half of making it from sizes.
+        need = need, cache.lens[:1].view(torch.float32).expand(shape[:3])
         if len(cache._need) < 4096:
             cache._need[key] = need
     s = _kv4_raw_stream(cache)
@@ -685,12 +687,12 @@ def sparstar_kv4_attn(cache: Kv4Cache, q, seqs=None, tau: float = None, causal: 
     if lse is not None:
         lp = _kv4_tensor(cache, lse, "lse", torch.float32, shape[:3])
     elif want_lse:
-        lse = torch.empty(shape[:3], dtype=torch.float32, device=cache.device)
+        lse = torch.empty_like(need[1], memory_format=torch.contiguous_format)
         lp = lse.data_ptr()
     else:
         lp = None
     if work is None:
-        work = cache._attn_work(need, s)
+        work = cache._attn_work(need[0], s)
     elif work.dtype is not torch.uint8 or work.get_device() != cache.index \
             or not work.is_contiguous():
         raise ValueError("work must be contiguous uint8 on %s" % cache.device)
