@@ -350,7 +350,8 @@ __global__ void __launch_bounds__(256) unpack_kernel(Kv4 c, Kv4Attn a, Plan p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         code[i] = __ldg(reinterpret_cast<const uint4 *>(half) + (32 * w + 8 * i + q) * 4 + g);
-    uint8_t *tile = p.tiles + (int64_t)blockIdx.x * kPairBytes + (values ? kTileBytes : 0);
+    extern __shared__ __align__(128) uint8_t pair[];
+    uint8_t *tile = pair + (values ? kTileBytes : 0);
     auto put = [&](uint32_t at, const uint4 &v) { *reinterpret_cast<uint4 *>(tile + at) = v; };
     const Unpack u(lane);
     if (values) {
@@ -365,6 +366,18 @@ __global__ void __launch_bounds__(256) unpack_kernel(Kv4 c, Kv4Attn a, Plan p) {
         for (int i = 0; i < 4; ++i) scale[i] = __ldg(s + (32 * w + 8 * i + q) * 4 + g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) u.keys(code[i], scale[i], 4 * w + i, put);
+    }
+    // A warp's rows are 4 KB of each panel.
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane < 2) {
+        const int at = (values ? kTileBytes : 0) + lane * kPanelBytes + w * 4096;
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                         p.tiles + (int64_t)blockIdx.x * kPairBytes + at),
+                     "r"(smem_addr(pair + at)), "r"(4096)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 }
 
@@ -1162,8 +1175,11 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
     const unsigned grid = (unsigned)(p.whole + tail * p.splits);
     if (first) {
         const int64_t tiles = (int64_t)a.n * c.max_pages * c.Hkv;
-        e = launch_after(unpack_kernel, (unsigned)(tiles + (p.chosen ? 1 : 0)), 256, 0, stream, c,
-                         a, p);
+        e = cudaFuncSetAttribute(unpack_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kPairBytes);
+        if (e == cudaSuccess)
+            e = launch_after(unpack_kernel, (unsigned)(tiles + (p.chosen ? 1 : 0)), 256,
+                             kPairBytes, stream, c, a, p);
         if (e != cudaSuccess) return e;
     }
     e = launch_after(kernel, grid, first ? kThreads<true> : kThreads<false>, kSmemBytes, stream,
