@@ -82,12 +82,15 @@ constexpr int kSmemBytes = kOffBar + (int)sizeof(Bars) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 constexpr uint32_t kIdesc = make_idesc(false);  // both operands K-major
 
-// Partial results of a CTA's rows, up to 256: maxima, sums, accumulators.
+// Partial results of a CTA's rows, up to 256: maxima, sums, and accumulators
+// as [kHD / 4][kBlock] fours, which the threads, a row each, store side by side.
 constexpr int kPartFloats = kBlock * (kHD + 2);  // a query block
 constexpr int kMaxParts = 4 * 148;  // units x splits, bounds the scratch
 constexpr int kMaxSplits = 16;
-// Scratch: the other kernel's zeros, the chosen chunk, the parts, the tiles.
-constexpr int kHeadBytes = SPARSTAR_KV4_WORK_ZEROS + 1024;
+// Scratch: the other kernel's zeros, the chosen chunk, what the joining kernel
+// needs to know of each split unit, the parts, the tiles.
+constexpr int kChosenBytes = 1024;
+constexpr int kHeadBytes = SPARSTAR_KV4_WORK_ZEROS + kChosenBytes + kMaxParts * 16;
 
 struct Plan {
     int heads;      // query heads a key head
@@ -101,6 +104,7 @@ struct Plan {
     int32_t *chosen;  // unpacked first, without lists: the chunk that the lengths ask for,
                       // then the sequences in order
     float sc;       // tau in log2 units, positive
+    int4 *split_units;  // of each unit behind `whole`: parts, stripe, first query block
     int join_rows;  // rows a CTA of the joining kernel
     float *parts;
     uint8_t *tiles;  // unpacked first: [sequence][block][head] pairs of tiles
@@ -403,6 +407,8 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
     const bool lists = a.kv_cnt != nullptr;
     if (un.slot < 0 && threadIdx.x == 0) kv4_flag(status, SPARSTAR_STATUS_BAD_INDEX);
     if (split >= un.parts) return;
+    if (p.splits > 1 && tail >= 0 && split == 0 && threadIdx.x == 0)
+        p.split_units[tail / p.splits] = make_int4(un.parts, stripe, qb0, 0);
     const bool joins = un.parts > 1;  // the result goes to `parts`
     Walk walk[2];
     {
@@ -947,7 +953,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         const int64_t out_row = (int64_t)stripe * p.rows + grow;
         float *part = p.parts + (int64_t)(joins ? tail * kBlocks<kPre> + (kPre ? x : 0) : 0) *
                                     kPartFloats;
-        float *part_o = part + 2 * kBlock + (int64_t)row * kHD;
+        uint4 *part_o = reinterpret_cast<uint4 *>(part + 2 * kBlock) + row;
         // A row without a weight (no token seen) gets 0.
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         if (kPre || x == 0) {
@@ -976,7 +982,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 if (joins) {
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
-                        reinterpret_cast<uint4 *>(part_o + 32 * q)[u] =
+                        part_o[(8 * q + u) * kBlock] =
                             make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
                 } else {
                     uint4 *o4 = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
@@ -1013,51 +1019,64 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
     }
 }
 
-// Joins the parts of every row, in order: a warp a row, four channels a lane.
-// All maxima and sums at once (one a lane), then eight accumulators a step.
-__global__ void __launch_bounds__(256) many_join_kernel(Kv4 c, Kv4Attn a, Plan p) {
+// Joins the parts of every row, in order: the weights first (a row and part a
+// thread), then eight rows a step, four channels of one a thread.  Eight rows
+// side by side are 128 bytes of a part; 32 bytes of a row's result are stored
+// together.
+__global__ void __launch_bounds__(256) many_join_kernel(Kv4Attn a, Plan p) {
+    constexpr int kMostRows = 32;
+    __shared__ float weight[kMostRows][kMaxSplits + 1], inverse[kMostRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.blocks * kBlock;  // of a unit
     const int at = blockIdx.x / (rows / p.join_rows);
+    const int r0 = blockIdx.x % (rows / p.join_rows) * p.join_rows;  // within one block
     kv4_begin();
-    const Unit u = unit_of(c, a, p, p.whole + at);
-    if (u.parts == 1) return;
-    const int n = u.parts;  // <= kMaxSplits
-    const float *first = p.parts + (int64_t)at * p.splits * p.blocks * kPartFloats;
-#pragma unroll 2
-    for (int i = 0; i < p.join_rows / 8; ++i) {
-        const int r0 = blockIdx.x % (rows / p.join_rows) * p.join_rows + i * 8 + warp;
-        const int srow = u.qb0 * kBlock + r0;
-        if (srow >= p.rows) break;
-        const int row = r0 % kBlock;
-        auto record = [&](int k) {
-            return first + ((int64_t)k * p.blocks + r0 / kBlock) * kPartFloats;
-        };
+    const int4 u = __ldcg(p.split_units + at);
+    const int n = u.x, srow0 = u.z * kBlock + r0;  // n <= kMaxSplits
+    if (n == 1 || srow0 >= p.rows) return;
+    const int64_t out0 = (int64_t)u.y * p.rows + srow0;
+    const float *first =
+        p.parts + ((int64_t)at * p.splits * p.blocks + r0 / kBlock) * kPartFloats;
+    const int row0 = r0 % kBlock;
+    const int64_t step = (int64_t)p.blocks * kPartFloats;
+    static_assert(kMaxSplits == 16, "half a warp a row");
+    for (int r = threadIdx.x / 16; r < p.join_rows; r += 16) {
+        const int k = threadIdx.x % 16;
         float m = -INFINITY, l = 0.0f;
-        if (lane < n) {
-            const float *rec = record(lane);
-            m = rec[row], l = rec[kBlock + row];
+        if (k < n) {
+            const float *rec = first + k * step + row0 + r;
+            m = rec[0], l = rec[kBlock];
         }
         float top = m;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float f = m > -INFINITY ? ex2(m - top) : 0.0f;
         float sum = f * l;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        weight[r][k] = f;
+        if (k > 0) continue;
+        inverse[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (a.lse && srow0 + r < p.rows)
+            a.lse[out0 + r] = (top + log2f(sum)) * 0.6931471805599453f;
+    }
+    __syncthreads();
+    const int four = warp * 4 + lane / 8;
+#pragma unroll 2
+    for (int r = lane % 8; r < p.join_rows; r += 8) {
+        if (srow0 + r >= p.rows) break;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 *src =
+            reinterpret_cast<const float4 *>(first + 2 * kBlock) + four * kBlock + row0 + r;
         for (int k0 = 0; k0 < n; k0 += 8) {
             float4 x[8];
             float w[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                w[k] = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+                w[k] = k0 + k < n ? weight[r][k0 + k] : 0.0f;
                 x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 // Parts without a seen token have stored nothing.
-                if (k0 + k < n && w[k] != 0.0f)
-                    x[k] = *(reinterpret_cast<const float4 *>(record(k0 + k) + 2 * kBlock +
-                                                              row * kHD) +
-                             lane);
+                if (w[k] != 0.0f) x[k] = src[(k0 + k) * step / 4];
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -1065,11 +1084,9 @@ __global__ void __launch_bounds__(256) many_join_kernel(Kv4 c, Kv4Attn a, Plan p
                 acc.z = fmaf(w[k], x[k].z, acc.z), acc.w = fmaf(w[k], x[k].w, acc.w);
             }
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const int64_t out_row = (int64_t)u.stripe * p.rows + srow;
-        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * kHD)[lane] =
+        const float inv = inverse[r];
+        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + (out0 + r) * kHD)[four] =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-        if (lane == 0 && a.lse) a.lse[out_row] = (top + log2f(sum)) * 0.6931471805599453f;
     }
 }
 
@@ -1164,6 +1181,8 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
                    ? static_cast<int32_t *>(a.work) + SPARSTAR_KV4_WORK_ZEROS / 4
                    : nullptr;
     p.sc = a.tau * 1.4426950408889634f;
+    p.split_units = reinterpret_cast<int4 *>(static_cast<uint8_t *>(a.work) +
+                                             SPARSTAR_KV4_WORK_ZEROS + kChosenBytes);
     p.parts = static_cast<float *>(a.work) + kHeadBytes / 4;
     p.tiles = static_cast<uint8_t *>(a.work) + kHeadBytes + part_bytes(s);
     p.tile_blocks = c.max_pages;
@@ -1189,7 +1208,7 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
     // their unit once.
     const int64_t rows = tail * p.blocks * kBlock;
     p.join_rows = rows / 8 <= 148 * 8 ? 8 : 32;
-    return launch_after(many_join_kernel, (unsigned)(rows / p.join_rows), 256, 0, stream, c, a, p);
+    return launch_after(many_join_kernel, (unsigned)(rows / p.join_rows), 256, 0, stream, a, p);
 }
 
 }  // namespace sparstar
