@@ -201,16 +201,16 @@ __device__ Unit unit_of(const Kv4 &c, const Kv4Attn &a, const Plan &p, int unit)
 }
 
 // The cost of a call whose units' pages are cut into chunks, in steps of a
-// pair of blocks over one page (1.9 us): a CTA takes about four steps beside
-// its pages, and four more to store 133 KB where the results are joined,
-// which reads them at 0.02 steps a CTA.  Equal CTAs run in waves; unequal
+// pair of blocks over one page (1.55 us): a CTA takes about four steps beside
+// its pages, and 1.5 more to store 133 KB where the results are joined, which
+// takes 2.5 and 0.01 a CTA.  Equal CTAs run in waves; unequal
 // ones follow each other and end about half a chunk apart.
 __host__ __device__ inline float cost_of(float ctas, float chunk, float steps, bool joins,
                                          bool equal) {
-    const float own = chunk + (joins ? 8.0f : 4.0f);
-    const float join = joins ? 3.0f + 0.02f * ctas : 0.0f;
+    const float own = chunk + (joins ? 5.5f : 4.0f);
+    const float join = joins ? 2.5f + 0.01f * ctas : 0.0f;
     if (equal || ctas <= 148.0f) return ceilf(ctas / 148.0f) * own + join;
-    const float packed = (steps + (joins ? 8.0f : 4.0f) * ctas) / 148.0f + 0.5f * chunk;
+    const float packed = (steps + (joins ? 5.5f : 4.0f) * ctas) / 148.0f + 0.5f * chunk;
     return fmaxf(own, packed) + join;
 }
 
@@ -1104,32 +1104,37 @@ Shape shape_of(const Kv4Shape &k, int64_t blocks) {
     return s;
 }
 
-// How a call's units are cut.  Where the device chooses the chunk: as many
-// CTAs a unit as the scratch holds.  Else, for units of equal length: whole
-// units in full waves first, the others split, as cheap as that gets.
-constexpr float kInPlaceStep = 0.85f;
-constexpr int kInPlaceBlocks = 4;
+// How a call's units are cut, and what that costs, in the steps of cost_of.
+// Where the device chooses the chunk: as many CTAs a unit as the scratch
+// holds.  Else, for units of equal length: whole units in full waves first,
+// the others split, as cheap as that gets.  `step`: what a step takes.
+constexpr float kInPlaceStep = 1.05f;  // one block over a page unpacked in place: 1.6 us
 struct Cut {
     int whole, splits;
+    float cost;
 };
-// `step`: what a step takes, in the steps of cost_of.
 Cut cut_of(int64_t units, int64_t tiles, float step, bool device_chooses) {
-    Cut best{0, 1};
-    float least = 0.0f;
-    for (int64_t whole = 0; whole <= units; whole += 148) {
-        if (whole > 0 && device_chooses) break;
+    Cut best{0, 1, cost_of((float)units, step * (float)tiles, 0.0f, false, true)};
+    const int64_t split = kMaxParts / 2;  // units that can be split at all
+    int64_t whole = units > split ? ceil_div(units - split, 148) * 148 : 0;
+    if (device_chooses) whole = 0;
+    for (; whole < units; whole += 148) {
+        const int64_t tail = units - whole;
         const float waves = (float)(whole / 148) * (step * (float)tiles + 4.0f);
-        for (int s = 1; s <= kMaxSplits; ++s) {
-            if (s > 1 && ((units - whole) * s > kMaxParts || tiles < 2 * s)) break;
-            const float cost =
-                waves + cost_of((float)((units - whole) * s),
-                                step * (float)ceil_div(tiles, s), 0.0f, s > 1, true);
-            if ((whole == 0 && s == 1) || device_chooses || cost < least)
-                best = Cut{(int)whole, s}, least = cost;
+        for (int s = 2; s <= kMaxSplits && tail * s <= kMaxParts && tiles >= 2 * s; ++s) {
+            const float cost = waves + cost_of((float)(tail * s), step * (float)ceil_div(tiles, s),
+                                               0.0f, true, true);
+            if (device_chooses || cost < best.cost)
+                best = Cut{(int)whole, s, cost < best.cost ? cost : best.cost};
         }
+        if (device_chooses) break;
     }
     return best;
 }
+bool chooses(const Kv4Shape &k, const Shape &s, bool causal) {
+    return !k.lists && (k.n > 1 || causal) && k.n * s.per <= kChosenUnits;
+}
+int64_t entries_of(const Kv4Shape &k) { return k.lists ? k.max_sel : k.max_pages; }
 
 // Scratch for the parts of a call, however it is cut.
 int64_t part_bytes(const Shape &s) {
@@ -1137,15 +1142,18 @@ int64_t part_bytes(const Shape &s) {
     return (parts < kMaxParts ? parts : kMaxParts) * s.blocks * kPartFloats * 4;
 }
 
-// Whether the pages are unpacked first.  That costs 22 ns a page and head
-// (measured, over the whole GPU) and makes a visit of a page by a query block
-// 7 ns; unpacking in place takes 8 to 16.
+// Whether the pages are unpacked first: what both ways cost for sequences that
+// fill their tables.  Unpacking takes 14 ns a page and head over the whole GPU,
+// and one more launch.  Measured, first against in place, 16 heads of one
+// sequence: 384 rows a head 92 against 86 us (16,512 tokens) and 34 against 32
+// (4,000); 512 rows 96 against 123 and 36 against 41; 1,000 rows 148 against
+// 224 and 54 against 62; 128 rows 62 against 41.
 bool unpack_first(const Kv4Shape &k) {
-    if (k.n * k.max_pages * k.Hkv * kPairBytes > ((int64_t)2 << 30)) return false;
-    const int64_t blocks = shape_of(k, 1).per;  // query blocks of a stripe
-    if (!k.lists) return blocks > kInPlaceBlocks;
-    return (double)(k.Hq / k.Hkv) * (double)blocks * (double)k.max_sel >
-           (double)kInPlaceBlocks * (double)k.max_pages;
+    const int64_t tiles = k.n * k.max_pages * k.Hkv;
+    if (tiles * kPairBytes > ((int64_t)2 << 30)) return false;
+    const Cut in_place = cut_of(shape_of(k, 1).units(), entries_of(k), kInPlaceStep, false);
+    const Cut first = cut_of(shape_of(k, 2).units(), entries_of(k), 1.0f, false);
+    return first.cost + 1.5f + 0.009f * (float)tiles < in_place.cost;
 }
 
 }  // namespace
@@ -1170,14 +1178,12 @@ cudaError_t launch_kv4_attn_many(const Kv4 &c, const Kv4Attn &a, const Kv4Shape 
     p.blocks = (int)s.blocks;
     p.per = (int)s.per;
     p.nqb = (int)ceil_div(s.rows, kBlock);
-    const int64_t entries = k.lists ? a.max_sel : c.max_pages;  // of a unit, at most
-    const bool chooses =
-        first && !k.lists && (a.n > 1 || a.causal) && a.n * s.per <= kChosenUnits;
-    // A step over a page unpacked in place: one block, 1.2 us.
-    const Cut cut = cut_of(s.units(), entries, first ? 1.0f : kInPlaceStep, chooses);
+    const int64_t entries = entries_of(k);  // of a unit, at most
+    const bool chosen = first && chooses(k, s, a.causal);
+    const Cut cut = cut_of(s.units(), entries, first ? 1.0f : kInPlaceStep, chosen);
     p.whole = cut.whole, p.splits = cut.splits;
     p.chunk = (int)ceil_div(entries > 0 ? entries : 1, p.splits);
-    p.chosen = chooses && p.splits > 1
+    p.chosen = chosen && p.splits > 1
                    ? static_cast<int32_t *>(a.work) + SPARSTAR_KV4_WORK_ZEROS / 4
                    : nullptr;
     p.sc = a.tau * 1.4426950408889634f;
