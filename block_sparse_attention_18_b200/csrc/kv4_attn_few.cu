@@ -7,16 +7,16 @@
 // a stripe.  Its work is one tile a page.
 //
 // Split.  All units' tiles form one line, cut into equal parts for 148 CTAs
-// and again for their eight warps: lengths from 1 to 144,512 tokens in one
-// batch keep every warp equally busy, and one long sequence is spread over
-// the whole GPU.  A warp's part may begin and end inside a unit; such partial
-// results (running maximum, sum, accumulator) are joined inside the CTA in
-// shared memory and across CTAs by a second kernel, always in the order of
-// the line, so results do not depend on timing.
+// and again for the parts of a CTA, a warp or a pair of warps each: lengths
+// from 1 to 144,512 tokens in one batch keep every warp equally busy, and one
+// long sequence is spread over the whole GPU.  A part may begin and end inside
+// a unit; such partial results (running maximum, sum, accumulator) are joined
+// inside the CTA in shared memory, and across CTAs by the last one to arrive,
+// always in the order of the line, so results do not depend on timing.
 //
-// Tile.  Each warp has its own ring of half pages (codes and scales of the
-// keys, or of the values), filled by one bulk copy each and waited for by
-// this warp alone.  Both products run on mma.m16n8k16 with the cache as the
+// Tile.  Each part has its own ring of half pages (codes and scales of the
+// keys, or of the values), filled by one bulk copy each and waited for by its
+// own warps alone.  Both products run on mma.m16n8k16 with the cache as the
 // 16-row operand and the query rows as the 8 columns: S^T = K q^T (16 tokens
 // x 8 rows) and O^T = V^T P^T (16 channels x 8 rows), so one dequantised
 // fragment serves all NT column tiles, and few rows waste no tensor work.
@@ -30,6 +30,15 @@
 // (kv4_dequant), so the cache adds no rounding.  fp32 queries and weights
 // are split into three bf16 terms each, whose sum is exact to 2^-24, and
 // multiplied term by term.
+//
+// Bounds.  The bytes of the pages at HBM's rate, in principle.  A page and head
+// costs a warp some 2,800 instructions, mostly on the integer pipe, of which
+// the twelve warps that the registers allow keep 58% busy: 18,064 pages and
+// heads (144,512 tokens, 16 heads, 315 MB) take 83 us, 3.8 TB/s, each further
+// one 3.4 ns, 5.1 TB/s.  Without the products it is 168 us of 177 at twice that
+// length, without the dequantisation's fma 146, without both 113.  A short line
+// is bound by the latencies in a row: 1 us to find the line, 1.5 the tiles, 1
+// the copy, 1.6 a page's arithmetic, 3 the joins; 897 tokens take 11.3 us.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -410,12 +419,17 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         if (a.lse)
             for (int64_t k = threadIdx.x; k < rows; k += kThreads) a.lse[i * rows + k] = -INFINITY;
     }
-    // This part: an equal piece of the CTA's tiles, the first ones a tile
-    // longer; parts with tiles are neighbours.
+    // This part: an equal piece of the CTA's tiles or, of one warp, half tiles,
+    // the first ones one longer; parts with tiles are neighbours, and two may
+    // have a half each of one tile.
+    constexpr uint32_t kCut = kPair > 1 ? 1 : 2;
     const int64_t c0 = min(share * blockIdx.x, total), c1 = min(c0 + share, total);
-    const uint32_t piece = (uint32_t)(c1 - c0) / kParts, rest = (uint32_t)(c1 - c0) % kParts;
-    const int64_t start = c0 + (int64_t)piece * part + min((uint32_t)part, rest);
-    const int x1 = (int)(piece + ((uint32_t)part < rest ? 1 : 0));  // tiles of the part
+    const uint32_t pieces = kCut * (uint32_t)(c1 - c0), each = pieces / kParts,
+                   rest = pieces % kParts;
+    const uint32_t h0 = each * part + min((uint32_t)part, rest);
+    const uint32_t h1 = h0 + each + ((uint32_t)part < rest ? 1 : 0);
+    const int64_t start = c0 + h0 / kCut;
+    const int x1 = h1 > h0 ? (int)((h1 + kCut - 1) / kCut - h0 / kCut) : 0;  // tiles of the part
     int x = 0;
     const int slot_id = blockIdx.x * kParts + part;
     uint8_t *ring = smem + part * kStages * kHalf;
@@ -500,7 +514,11 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         const bool t_has = (has >> at) & 1u;
         // block and edge in one word
         const int t_meta = __shfl_sync(0xffffffffu, now.block * 4 + now.edge, at);
-        const int t_block = t_meta >> 2, t_edge = t_meta & 3;
+        const int t_block = t_meta >> 2;
+        // The halves of the tile that are this part's, and its unit's edges there.
+        const int hp0 = kCut > 1 && x == 0 ? (int)(h0 % kCut) : 0;
+        const int hp1 = kCut > 1 && x + 1 == x1 ? 2 - (int)(h1 % kCut) : 2;
+        const int t_edge = t_meta & ((hp0 == 0 ? 1 : 0) | (hp1 == 2 ? 2 : 0));
         if (uid < 0) {  // a unit begins (the one before it has been stored)
             uid = __shfl_sync(0xffffffffu, now.uid, at);
             started = t_edge & 1;
@@ -558,7 +576,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
             // loop is kept, as the whole page's code would not fit the
             // instruction cache.
 #pragma unroll 1
-            for (int hp = kPair > 1 ? member : 0; hp < (kPair > 1 ? member + 1 : 2); ++hp) {
+            for (int hp = kPair > 1 ? member : hp0; hp < (kPair > 1 ? member + 1 : hp1); ++hp) {
                 float s[4][NT][4];
                 // ------------------------------------------ S^T = K q^T
                 // Two token tiles at a time: two chains of products.
@@ -611,7 +629,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
                                     mma(s[u0 + d][nt], f, q[t][nt][k][0], q[t][nt][k][1]);
                         }
                 }
-                if (kPair > 1 || hp == 1) release();  // the keys
+                if (kPair > 1 || hp + 1 == hp1) release();  // the keys
                 // --------------------------------------------- softmax
                 if ((t_block + 1) * kBlock > seen_min) {
 #pragma unroll
@@ -670,7 +688,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
                     }
                 }
                 // ------------------------------------- O^T += V^T P^T
-                if (kPair > 1 || hp == 0) {
+                if (kPair > 1 || hp == hp0) {
                     ok = ok && wait_warp(&full[part][sv], pv);
                     if (!ok) break;
                 }
@@ -1026,23 +1044,24 @@ cudaError_t launch_kv4_attn_few(const Kv4 &c, const Kv4Attn &a, int dtype, cudaS
     p.arrived = static_cast<uint32_t *>(a.work);
     p.joins = static_cast<float *>(a.work) + kArrivedBytes / 4;
     p.ends = p.joins + (int64_t)2 * kCtas * R * (c.D + 2);
-    // Eight rows: twelve warps, each with pages of its own, keep the registers
-    // that hide the latencies.  Where every CTA gets a few tiles at most, eight
-    // pairs of warps, each half of a page: the tokens of a page are dealt with
-    // in half the time (897 tokens, 16 heads: 13.5 us against 15.2; 144,000
-    // tokens: 98 against 89).
-    const bool short_line = (double)a.n * p.units * (lists ? a.max_sel : c.max_pages) <=
-                            8.0 * kCtas;
+    // Eight rows: twelve warps, each with (halves of) pages of its own, keep the
+    // registers that hide the latencies.  Where that gives some warps one half
+    // and some two or three, eight pairs of warps, each a page at a time, take
+    // less (16 heads: 6,000 tokens 14.1 us against 17.0, 9,000 tokens 15.7
+    // against 18.9; below, 1,000 tokens, 12.0 against 11.3, and above, 15,000
+    // tokens, 23.8 against 22.6).
+    const double most = (double)a.n * p.units * (lists ? a.max_sel : c.max_pages);
+    const bool pairs = most > 2.0 * kCtas && most <= 8.0 * kCtas;
     if (c.D == 128) {
         if (f32) return launch<128, 1, true, 8, 1>(c, a, p, stream);
         if (R == 16) return launch<128, 2, false, 8, 1>(c, a, p, stream);
-        return short_line ? launch<128, 1, false, 8, 2>(c, a, p, stream)
-                          : launch<128, 1, false, 12, 1>(c, a, p, stream);
+        return pairs ? launch<128, 1, false, 8, 2>(c, a, p, stream)
+                     : launch<128, 1, false, 12, 1>(c, a, p, stream);
     }
     if (f32) return launch<64, 1, true, 8, 1>(c, a, p, stream);
     if (R == 16) return launch<64, 2, false, 8, 1>(c, a, p, stream);
-    return short_line ? launch<64, 1, false, 8, 2>(c, a, p, stream)
-                      : launch<64, 1, false, 12, 1>(c, a, p, stream);
+    return pairs ? launch<64, 1, false, 8, 2>(c, a, p, stream)
+                 : launch<64, 1, false, 12, 1>(c, a, p, stream);
 }
 
 }  // namespace sparstar
