@@ -35,8 +35,9 @@
 // costs a warp some 2,800 instructions, mostly on the integer pipe, of which
 // the twelve warps that the registers allow keep 58% busy: 18,064 pages and
 // heads (144,512 tokens, 16 heads, 315 MB) take 83 us, 3.8 TB/s, each further
-// one 3.4 ns, 5.1 TB/s.  Without the products it is 168 us of 177 at twice that
-// length, without the dequantisation's fma 146, without both 113.  A short line
+// one 3.4 ns, 5.1 TB/s.  At twice that length it takes 144 us, and the copies
+// alone 113; without the products or without the extraction of codes hardly
+// less, without the dequantisation's fma a sixth less.  A short line
 // is bound by the latencies in a row: 1 us to find the line, 1.5 the tiles, 1
 // the copy, 1.6 a page's arithmetic, 3 the joins; 897 tokens take 11.3 us.
 #include <cuda_bf16.h>
@@ -47,7 +48,7 @@ namespace sparstar {
 namespace {
 
 constexpr int kCtas = 148;
-constexpr int kEndRows = 128;  // rows of a CTA's parts and warps, all of them
+constexpr int kEndRows = 128;  // rows of a CTA's warps, all of them
 constexpr int kArrivedBytes = SPARSTAR_KV4_WORK_ZEROS;  // kCtas words and alignment
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kChunks = 256;  // of sequences, for finding a place on the line
