@@ -603,8 +603,10 @@ def sparstar_kv4_read(cache: Kv4Cache, T: int, n: int = None, dtype=torch.bfloat
                       starts=None, counts=None, k=None, v=None, status=None, stream=None):
     """The values of T tokens of each of n sequences; returns (k, v)
     [n, Hkv, T, D].  Rows beyond counts are not written (buffers that the
-    call allocates hold zeros there).  n, unless given, follows from seqs,
-    starts, counts, k or v, and is every sequence without them."""
+    call allocates hold zeros there), nor are those of entries that are left
+    out (status; undefined in such buffers where counts is not given).  n,
+    unless given, follows from seqs, starts, counts, k or v, and is every
+    sequence without them."""
     if _kv4_elsewhere(cache, stream):
         with _Kv4There(cache, stream):
             return sparstar_kv4_read(cache, T, n, dtype, seqs, starts, counts, k, v, status)

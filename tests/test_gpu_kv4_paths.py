@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from kv4_ref import BLOCK
+from kv4_ref import BAD_INDEX, BLOCK
 from test_gpu_kv4 import (BF16, F32, check_attn, check_state, filled, ints, model, new_status,
                           queries, sp, status_of, tokens)  # noqa: F401
 
@@ -248,3 +248,52 @@ def test_a_run_of_calls_without_pauses(sp):
         assert (np.abs(out.double().cpu().numpy() - want[0]) <= tol * 1.01).all()
     check_state(cache, ref)
     assert status_of(status) == ref.status == 0
+
+
+def test_page_calls_captured_into_a_graph(sp):
+    """Free, fork both ways, grow and compact, replayed over tables that the
+    replay before changed, against the model."""
+    cache = filled(sp, [700, 0, 0, 130], 1, 64, max_pages=8, extra=20)
+    status, n_live = new_status(), ints(0)
+    src, dst, deep = ints(0, 3), ints(1, 2), ints(1)
+    lens = ints(650, 130)
+    none, grown, first = ints(0, 0), ints(655, 135), ints(0)
+    ref = model(cache)
+
+    def calls(c):
+        c("resize", none, dst)
+        c("fork", src[1:], dst[:1], lens[1:], False)
+        c("resize", first, deep)
+        c("fork", src, dst, lens, False)
+        c("resize", grown, dst)
+        c("resize", none, dst)
+        c("fork", src, dst, lens, True)
+        c("compact")
+
+    def on_gpu(name, *args):
+        if name == "resize":
+            sp.sparstar_kv4_resize(cache, *args, status=status)
+        elif name == "fork":
+            sp.sparstar_kv4_fork(cache, *args, status=status)
+        else:
+            sp.sparstar_kv4_compact(cache, n_live)
+
+    def on_model(name, *args):
+        args = [x.cpu().numpy() if torch.is_tensor(x) else x for x in args]
+        if name == "compact":
+            assert int(n_live) == ref.compact()
+        else:
+            getattr(ref, name)(*args)
+
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        calls(on_gpu)
+    for step in range(4):
+        g.replay()
+        torch.cuda.synchronize()
+        calls(on_model)
+        check_state(cache, ref, "replay %d" % step)
+        # 655 + 3 * 128 tokens are more than eight pages hold.
+        assert status_of(status) == ref.status == (BAD_INDEX if step == 3 else 0)
+        grown.add_(128)
