@@ -115,7 +115,7 @@ struct Plan {
     int4 *split_units;  // of each unit behind `whole`: parts, stripe, first query block
     int join_rows;  // rows a CTA of the joining kernel
     float *parts;
-    uint8_t *tiles;  // unpacked first: [sequence][block][head] pairs of tiles
+    uint8_t *tiles;  // unpacked first: [sequence][head][block] pairs of tiles
     int tile_blocks;
 };
 constexpr int kPairBytes = 2 * kTileBytes;  // a page's keys, then its values
@@ -387,7 +387,8 @@ __global__ void __launch_bounds__(256) unpack_kernel(Kv4 c, Kv4Attn a, Plan p) {
     if (lane < 2) {
         const int at = (values ? kTileBytes : 0) + lane * kPanelBytes + w * 4096;
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                         p.tiles + (int64_t)blockIdx.x * kPairBytes + at),
+                         p.tiles +
+                         (((int64_t)seq * c.Hkv + kh) * p.tile_blocks + block) * kPairBytes + at),
                      "r"(smem_addr(pair + at)), "r"(4096)
                      : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -594,23 +595,54 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         if (lane == 0 && nmax > 0) {
             load_q();
             const uint8_t *tiles =
-                p.tiles + ((int64_t)seq * p.tile_blocks * c.Hkv + kh) * kPairBytes;
-            int e = 0, page;
-            for (int tile = next_tile(); tile >= 0; tile = next_tile()) {
-                const int block = find(tile, page);
+                p.tiles + ((int64_t)seq * c.Hkv + kh) * p.tile_blocks * kPairBytes;
+            // The blocks of a stream: the next key tile's, looked up ahead, the
+            // last key tile's and the one before, whose values follow.
+            struct Stream {
+                const Walk &w;
+                const bool every;  // each entry counts
+                int cur, next, last, before;
+                __device__ Stream(const Walk &w, int n)
+                    : w(w), every(n == w.hi - w.lo), cur(w.lo), last(0), before(0) {
+                    next = ahead();
+                }
+                __device__ int ahead() {
+                    int page;
+                    if (!every) return w.next(cur, page);
+                    const int at = cur < w.hi ? cur++ : cur;
+                    return w.list && at < w.hi ? __ldg(w.list + at) : at;
+                }
+                __device__ int key() {
+                    before = last, last = next;
+                    next = ahead();
+                    return last;
+                }
+            };
+            Stream A(wa, sA), B(wb, sB);
+            int e = 0;
+            bool ok = true;
+            auto load = [&](int block, int is_v) {
+                if (!ok) return;
                 const int stage = e % kStages;
-                if (!wait1(bar_empty(stage), ((uint32_t)(e / kStages) & 1u) ^ 1u, abort_flag,
-                           status))
-                    break;
+                ok = wait1(bar_empty(stage), ((uint32_t)(e / kStages) & 1u) ^ 1u, abort_flag,
+                           status);
+                if (!ok) return;
                 mbar_expect_tx(bar_full(e), kTileBytes);
-                const uint8_t *src = tiles + (int64_t)block * c.Hkv * kPairBytes +
-                                     (tile & 1) * kTileBytes;
+                const uint8_t *src = tiles + (int64_t)block * kPairBytes + is_v * kTileBytes;
                 asm volatile(
                     "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
                     "[%1], %2, [%3];" ::"r"(base + kOffStage + stage * kTileBytes),
                     "l"(src), "r"(kTileBytes), "r"(bar_full(e))
                     : "memory");
                 ++e;
+            };
+            if (sA > 0) load(A.key(), 0);
+            if (sB > 0) load(B.key(), 0);
+            for (int j = 0; j < max(sA, sB) && ok; ++j) {
+                if (j + 1 < sA) load(A.key(), 0);
+                if (j < sA) load(j + 1 < sA ? A.before : A.last, 1);
+                if (j + 1 < sB) load(B.key(), 0);
+                if (j < sB) load(j + 1 < sB ? B.before : B.last, 1);
             }
             // Copies in flight land before the CTA may exit.
             drain_wait(bar_q, 0);
