@@ -156,6 +156,36 @@ struct Walk {
     }
 };
 
+// The blocks (or pages) of a stream of tiles, for the copying lane: the next key
+// tile's, looked up ahead, the last key tile's and the one before, whose values
+// follow.  A lookup between two copies costs as much as a fifth of a step.
+template <bool kPages>
+struct Stream {
+    const Walk &w;
+    const bool every;  // each entry counts
+    int cur, next, last, before;
+    __device__ Stream(const Walk &w, int n)
+        : w(w), every(n == w.hi - w.lo), cur(w.lo), last(0), before(0) {
+        next = ahead();
+    }
+    __device__ int ahead() {
+        int page;
+        if (!every) {
+            const int block = w.next(cur, page);
+            return kPages ? page : block;
+        }
+        if (cur >= w.hi) return 0;
+        const int block = w.list ? __ldg(w.list + cur) : cur;
+        ++cur;
+        return kPages ? __ldg(w.table + block) : block;
+    }
+    __device__ int key() {
+        before = last, last = next;
+        next = ahead();
+        return last;
+    }
+};
+
 // Sequences that are put in order, units that are counted (choose_chunk).
 constexpr int kOrdered = 240, kChosenUnits = 1024;
 
@@ -527,12 +557,6 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             if (ph & 1 ? j < n : j + 1 < n) return (ph & 1) | (ph & 2);
         }
     };
-    int cur_k[2] = {wa.lo, wb.lo}, cur_v[2] = {wa.lo, wb.lo};
-    // The block of a tile; `page` its page.
-    auto find = [&](int tile, int &page) {
-        if (tile & 2) return wb.next(tile & 1 ? cur_v[1] : cur_k[1], page);
-        return wa.next(tile & 1 ? cur_v[0] : cur_k[0], page);
-    };
     auto bar_packed = [&](int s) { return smem_addr(&bars->packed_full[s]); };
     auto bar_unpacked = [&](int s) { return smem_addr(&bars->packed_empty[s]); };
     auto load_q = [&]() {  // by one lane
@@ -596,29 +620,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             load_q();
             const uint8_t *tiles =
                 p.tiles + ((int64_t)seq * c.Hkv + kh) * p.tile_blocks * kPairBytes;
-            // The blocks of a stream: the next key tile's, looked up ahead, the
-            // last key tile's and the one before, whose values follow.
-            struct Stream {
-                const Walk &w;
-                const bool every;  // each entry counts
-                int cur, next, last, before;
-                __device__ Stream(const Walk &w, int n)
-                    : w(w), every(n == w.hi - w.lo), cur(w.lo), last(0), before(0) {
-                    next = ahead();
-                }
-                __device__ int ahead() {
-                    int page;
-                    if (!every) return w.next(cur, page);
-                    const int at = cur < w.hi ? cur++ : cur;
-                    return w.list && at < w.hi ? __ldg(w.list + at) : at;
-                }
-                __device__ int key() {
-                    before = last, last = next;
-                    next = ahead();
-                    return last;
-                }
-            };
-            Stream A(wa, sA), B(wb, sB);
+            Stream<false> A(wa, sA), B(wb, sB);
             int e = 0;
             bool ok = true;
             auto load = [&](int block, int is_v) {
@@ -698,22 +700,29 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         if (lane == 0 && nmax > 0) {
             load_q();
             constexpr int kHalf = kv4_half_bytes(kHD);
-            int e = 0, page;
-            for (int tile = next_tile(); tile >= 0; tile = next_tile()) {
-                find(tile, page);
+            Stream<true> pages(walk[0], nA);
+            int e = 0;
+            bool ok = true;
+            auto load = [&](int page, int is_v) {
+                if (!ok) return;
                 const int s = e % kPackedStages;
-                if (!wait1(bar_unpacked(s), ((uint32_t)(e / kPackedStages) & 1u) ^ 1u,
-                           abort_flag, status))
-                    break;
+                ok = wait1(bar_unpacked(s), ((uint32_t)(e / kPackedStages) & 1u) ^ 1u, abort_flag,
+                           status);
+                if (!ok) return;
                 mbar_expect_tx(bar_packed(s), kHalf);
                 const uint8_t *src =
-                    c.pages + ((int64_t)page * c.Hkv + kh) * (2 * kHalf) + (tile & 1) * kHalf;
+                    c.pages + ((int64_t)page * c.Hkv + kh) * (2 * kHalf) + is_v * kHalf;
                 asm volatile(
                     "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
                     "[%1], %2, [%3];" ::"r"(base + kOffPacked + s * kHalf),
                     "l"(src), "r"(kHalf), "r"(bar_packed(s))
                     : "memory");
                 ++e;
+            };
+            load(pages.key(), 0);
+            for (int j = 0; j < nA && ok; ++j) {
+                if (j + 1 < nA) load(pages.key(), 0);
+                load(j + 1 < nA ? pages.before : pages.last, 1);
             }
             // Copies in flight land before the CTA may exit.
             drain_wait(bar_q, 0);
