@@ -537,26 +537,6 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
     auto k_slot = [&](int x, int j) { return slot_k(apart ? x : 0, j, sA, sB); };
     auto v_slot = [&](int x, int j) { return slot_v(apart ? x : 0, j, sA, sB); };
 
-    // The stream whose pages A and B share is the longer one.
-    const Walk wa = !kPre || apart || nA >= nB ? walk[0] : walk[1], wb = walk[1];
-    // Tiles in ring order: bit 0 values, bit 1 stream B; -1 after the last.
-    int step = -1, phase = 0;
-    auto next_tile = [&]() {
-        while (true) {
-            if (step < 0) {
-                const int ph = phase++;
-                if (phase == 2) step = 0, phase = 0;
-                if (ph == 0 ? sA > 0 : sB > 0) return ph << 1;
-                continue;
-            }
-            if (step >= (sA > sB ? sA : sB)) return -1;
-            const int ph = phase, j = step;
-            phase = (phase + 1) & 3;
-            if (phase == 0) ++step;
-            const int n = ph < 2 ? sA : sB;
-            if (ph & 1 ? j < n : j + 1 < n) return (ph & 1) | (ph & 2);
-        }
-    };
     auto bar_packed = [&](int s) { return smem_addr(&bars->packed_full[s]); };
     auto bar_unpacked = [&](int s) { return smem_addr(&bars->packed_empty[s]); };
     auto load_q = [&]() {  // by one lane
@@ -620,7 +600,9 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
             load_q();
             const uint8_t *tiles =
                 p.tiles + ((int64_t)seq * c.Hkv + kh) * p.tile_blocks * kPairBytes;
-            Stream<false> A(wa, sA), B(wb, sB);
+            // The stream whose pages A and B share is the longer one's.
+            const Walk wa = !apart && nB > nA ? walk[1] : walk[0];
+            Stream<false> A(wa, sA), B(walk[1], sB);
             int e = 0;
             bool ok = true;
             auto load = [&](int block, int is_v) {
@@ -788,8 +770,8 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         const int in_first = 4 - (strip0 & 3);  // strips of the first group
         const Unpack u(lane);
         constexpr int kHalf = kv4_half_bytes(kHD);
-        int e = 0;
-        for (int tile = next_tile(); tile >= 0; tile = next_tile(), ++e) {
+        for (int e = 0; e < 2 * nA; ++e) {  // K 0, K 1, V 0, K 2, V 1, .. V n - 1
+            const bool is_v = e > 0 && (e % 2 == 0 || e == 2 * nA - 1);
             const int s = e % kPackedStages, stage = e % kStages;
             if (!wait_warp(bar_packed(s), (uint32_t)(e / kPackedStages) & 1u, abort_flag, status))
                 break;
@@ -809,7 +791,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + at),
                              "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
             };
-            if (tile & 1) {
+            if (is_v) {
                 auto pairs_of = [&](int group, Unpack::Pairs &pairs) {
                     const uint4 *sv =
                         reinterpret_cast<const uint4 *>(scales + group * kBlock + 32 * g);
@@ -1159,7 +1141,7 @@ Shape shape_of(const Kv4Shape &k, int64_t blocks) {
 // Where the device chooses the chunk: as many CTAs a unit as the scratch
 // holds.  Else, for units of equal length: whole units in full waves first,
 // the others split, as cheap as that gets.  `step`: what a step takes.
-constexpr float kInPlaceStep = 1.05f;  // one block over a page unpacked in place: 1.6 us
+constexpr float kInPlaceStep = 0.92f;  // one block over a page unpacked in place: 1.43 us
 struct Cut {
     int whole, splits;
     float cost;
