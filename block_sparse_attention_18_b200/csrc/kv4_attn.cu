@@ -5,10 +5,11 @@ namespace sparstar {
 namespace {
 
 // Rows of a stripe from which the tcgen05 kernel, which multiplies 128 rows
-// whatever it is given, takes over from the other one's 8 or 16 at a time.
-// Measured, 8 key heads: at 32 rows 39 (few) against 38 us for four sequences
-// of 8,000 tokens and 68 against 75 for one of 72,000; at 40 rows 53 against 38
-// and 89 against 75.
+// whatever it is given, takes over from the other one's 8 or 16 at a time, each
+// of which unpacks the pages again.  Measured, 8 key heads, 17 to 32 rows (two
+// times 16): four sequences of 8,000 tokens 37 (few) against 35 us, one of
+// 72,000 67 against 67, 64 of 1,000 61 against 73; 40 rows, a third time more:
+// 53 and 89 against 35 and 67.
 constexpr int64_t kManyRows = 33;
 
 bool many(const Kv4Shape &s, float tau) {

@@ -11,8 +11,9 @@
 // from 1 to 144,512 tokens in one batch keep every warp equally busy, and one
 // long sequence is spread over the whole GPU.  A part may begin and end inside
 // a unit; such partial results (running maximum, sum, accumulator) are joined
-// inside the CTA in shared memory, and across CTAs by the last one to arrive,
-// always in the order of the line, so results do not depend on timing.
+// inside the CTA in shared memory, and across CTAs by the last one to arrive
+// (in groups first, where they are many), always in the order of the line, so
+// results do not depend on timing.
 //
 // Tile.  Each part has its own ring of half pages (codes and scales of the
 // keys, or of the values), filled by one bulk copy each and waited for by its
@@ -52,6 +53,10 @@ constexpr int kEndRows = 128;  // rows of a CTA's warps, all of them
 constexpr int kArrivedBytes = SPARSTAR_KV4_WORK_ZEROS;  // kCtas words and alignment
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kChunks = 256;  // of sequences, for finding a place on the line
+// A unit of more CTAs than kJoined is joined in groups of kFan first, as one CTA
+// takes long to read 148 partial results (72,000 tokens, one key head: eight
+// rows 22.9 us, so 16.6; sixteen rows 39.3 and 23.0).
+constexpr int kFan = 12, kJoined = 32;
 
 struct Plan {
     int heads;       // query heads a key head
@@ -60,8 +65,9 @@ struct Plan {
     int nqb;         // query blocks of a head (lists)
     float sc;        // |tau| in log2 units
     uint32_t flip;   // sign bits to flip in q (tau < 0)
-    uint32_t *arrived;  // [kCtas]: CTAs whose partial result of the unit that begins in this
-                        // CTA and goes on is stored; 0 between calls
+    uint32_t *arrived;  // [kCtas]: high half: CTAs (or groups) whose partial result of the
+                        // unit that begins in this CTA and goes on is stored; low half:
+                        // CTAs of the group that begins here; 0 between calls
     float *joins;       // [kCtas][2][R][D + 2]: a CTA's partial results: of the unit that
                         // goes on from the CTA before, of the one that begins here
     float *ends;        // [kCtas * kParts][kPair][R][D + 2]: ends of units inside a part
@@ -311,17 +317,30 @@ struct Part4 {
     }
 };
 
-// The result of a unit whose partial results are the records of CTAs from ..
-// to, joined in that order whichever CTA runs this.  A thread has four
-// channels of a row; spare threads take the records in pieces.  Eight records
-// a step: their loads overlap.
+// Counts one more arrival (from bit `shift`) and says whether all have arrived;
+// what their CTAs stored can then be read.  The last one sets the count back,
+// behind the fence: nobody waits for that.
+__device__ __forceinline__ bool arrive(uint32_t *count, int shift, int all) {
+    __threadfence();
+    const uint32_t before = atomicAdd(count, 1u << shift);
+    __threadfence();
+    const bool last = ((before >> shift) & 0xffffu) == (uint32_t)(all - 1);
+    if (last) atomicSub(count, (uint32_t)all << shift);
+    return last;
+}
+
+// The result of a unit whose partial results are the records of CTAs from,
+// from + step .. to (`begins`: the unit begins in the first), joined in that
+// order whichever CTA runs this; without `u` a record in the first one's place.
+// A thread has four channels of a row; spare threads take the records in
+// pieces.  Eight records a step: their loads overlap.
 template <typename T, int D, int R, int kThreads>
-__device__ void join(const Plan &p, int from, int to, const Unit &u, const Kv4Attn &a,
-                     float *shared) {
+__device__ void join(const Plan &p, int from, int to, int step, bool begins, const Unit *u,
+                     const Kv4Attn &a, float *shared) {
     constexpr int kRecord = R * (D + 2), kVecs = R * D / 4;
     constexpr int kSplit = kThreads > kVecs ? kThreads / kVecs : 1;
-    const int n = to - from + 1;
-    const float *first = p.joins + ((int64_t)2 * from + 1) * kRecord;
+    const int n = (to - from) / step + 1;
+    float *first = p.joins + ((int64_t)2 * from + (begins ? 1 : 0)) * kRecord;
     const float *later = p.joins + (int64_t)2 * from * kRecord;  // + 2 kRecord a CTA
     auto *piece = reinterpret_cast<Part4 *>(shared);             // [kSplit][kVecs]
     for (int v = threadIdx.x; v < kVecs * kSplit; v += kThreads) {
@@ -335,7 +354,7 @@ __device__ void join(const Plan &p, int from, int to, const Unit &u, const Kv4At
             for (int k = 0; k < 8; ++k) {
                 m[k] = -INFINITY, l[k] = 0.0f, x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (k0 + k >= k1) continue;
-                const float *rec = k0 + k ? later + (int64_t)(k0 + k) * 2 * kRecord : first;
+                const float *rec = k0 + k ? later + (int64_t)(k0 + k) * 2 * step * kRecord : first;
                 m[k] = __ldcg(rec + R * D + row);
                 l[k] = __ldcg(rec + R * D + R + row);
                 x[k] = __ldcg(reinterpret_cast<const float4 *>(rec) + vec);
@@ -351,7 +370,7 @@ __device__ void join(const Plan &p, int from, int to, const Unit &u, const Kv4At
     __syncthreads();
     for (int v = threadIdx.x; v < kVecs; v += kThreads) {
         const int row = v / (D / 4), d = v % (D / 4) * 4;
-        if (row >= u.rows) continue;
+        if (u && row >= u->rows) continue;
         Part4 part = piece[v];
 #pragma unroll
         for (int s = 1; s < kSplit; ++s) {
@@ -359,8 +378,13 @@ __device__ void join(const Plan &p, int from, int to, const Unit &u, const Kv4At
             part.scale(fmaxf(part.top, o.top));
             part.add(o.top, o.sum, o.acc);
         }
-        part.write(static_cast<T *>(a.out) + (u.row + row) * D + d,
-                   d == 0 && a.lse ? a.lse + u.row + row : nullptr);
+        if (u) {
+            part.write(static_cast<T *>(a.out) + (u->row + row) * D + d,
+                       d == 0 && a.lse ? a.lse + u->row + row : nullptr);
+        } else {
+            reinterpret_cast<float4 *>(first)[v] = part.acc;
+            if (d == 0) first[R * D + row] = part.top, first[R * D + R + row] = part.sum;
+        }
     }
 }
 
@@ -387,7 +411,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     __shared__ int32_t group_flags[2 * kParts], group_rows[2 * kParts];
     __shared__ uint32_t group_entries[2 * kParts];
     __shared__ int64_t group_row[2 * kParts];
-    __shared__ int32_t cross[2], span[2][2], n_cross, n_groups;
+    __shared__ int32_t cross[2], span[2][2], step[2], n_cross, n_groups;
     const int part = (threadIdx.x >> 5) / kPair, member = (threadIdx.x >> 5) % kPair;
     const int lane = threadIdx.x & 31;
     const int r = lane >> 2, j = lane & 3;
@@ -985,20 +1009,34 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     }
     // ---------------- units of several CTAs: the last one to arrive joins them
     __syncthreads();
+    const int me = blockIdx.x;
     if (threadIdx.x < n_cross) {
-        const int from = span[threadIdx.x][0], to = span[threadIdx.x][1];
-        __threadfence();
-        const bool last = atomicAdd(p.arrived + from, 1u) == (uint32_t)(to - from);
-        if (last) p.arrived[from] = 0;
-        __threadfence();
-        if (!last) span[threadIdx.x][0] = -1;
+        const int k = threadIdx.x, from = span[k][0], to = span[k][1];
+        const bool group = to - from >= kJoined;  // its group first
+        const int g0 = group ? me - (me - from) % kFan : from;
+        const int all = (group ? min(g0 + kFan - 1, to) : to) - g0 + 1;
+        const bool last = all == 1 || arrive(p.arrived + g0, group ? 0 : 16, all);
+        step[k] = last ? (group ? kFan : 1) : 0;
     }
     __syncthreads();
+    float *shared = reinterpret_cast<float *>(smem);
     for (int k = 0; k < n_cross; ++k) {
-        if (span[k][0] < 0) continue;
-        join<T, D, R, kThreads>(p, span[k][0], span[k][1], unit_of<R>(c, a, p, cross[k]), a,
-                                reinterpret_cast<float *>(smem));
-        __syncthreads();
+        if (step[k] == 0) continue;
+        const Unit un = unit_of<R>(c, a, p, cross[k]);
+        const int from = span[k][0], to = span[k][1], g0 = me - (me - from) % kFan;
+        bool group = step[k] == kFan;
+        while (true) {  // one copy of the code
+            const int r0 = group ? g0 : from, r1 = group ? min(g0 + kFan - 1, to) : to;
+            join<T, D, R, kThreads>(p, r0, r1, group ? 1 : step[k], !group || g0 == from,
+                                    group ? nullptr : &un, a, shared);
+            __syncthreads();
+            if (!group) break;
+            if (threadIdx.x == 0 && !arrive(p.arrived + from, 16, (to - from) / kFan + 1))
+                step[k] = 0;
+            __syncthreads();
+            if (step[k] == 0) break;
+            group = false;
+        }
     }
 }
 

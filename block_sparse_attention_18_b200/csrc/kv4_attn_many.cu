@@ -31,12 +31,12 @@
 // of its own joins the results, in order.
 //
 // Bounds.  Unpacked first: the tensor and the exponential units in turn, as in
-// attn_sm100.cu.  8,000 rows of 16 heads over 16,512 tokens, every block: 766
-// us, 1.41 PFLOP/s; over lists that keep 0.625 of them 619 us, 1.12 PFLOP/s, and
-// 28 to unpack 135 MB (26 at HBM's rate).  In place: the unpacking warps, 1.6 us
-// a page where the MMAs of one block need 0.5: 128 rows over 72,000 tokens, 16
-// heads, 128 us.  Short calls: about 14 us of start, epilogue and joining beside
-// the pages.
+// attn_sm100.cu.  8,000 rows of 16 heads over 16,512 tokens, every block: 760
+// us, 1.42 PFLOP/s; over lists of 83 of the 129 blocks 555 us, 1.25 PFLOP/s, as
+// long as attn_sm100.cu takes over the values themselves; 28 us of each unpack
+// 135 MB (26 at HBM's rate).  In place: the unpacking warps, 1.43 us a page where
+// the MMAs of one block need 0.5: 128 rows over 72,000 tokens, 16 heads, 113 us.
+// Short calls: about 14 us of start, epilogue and joining beside the pages.
 #include "kv4.cuh"
 #include "sm100.cuh"
 
@@ -94,7 +94,7 @@ constexpr uint32_t kIdesc = make_idesc(false);  // both operands K-major
 // as [kHD / 4][kBlock] fours, which the threads, a row each, store side by side.
 constexpr int kPartFloats = kBlock * (kHD + 2);  // a query block
 constexpr int kMaxParts = 4 * 148;  // units x splits, bounds the scratch
-constexpr int kMaxSplits = 16;
+constexpr int kMaxSplits = 64;
 // Scratch: the other kernel's zeros, the chosen chunk, what the joining kernel
 // needs to know of each split unit, the parts, the tiles.
 constexpr int kChosenBytes = 1024;
@@ -1072,23 +1072,32 @@ __global__ void __launch_bounds__(256) many_join_kernel(Kv4Attn a, Plan p) {
         p.parts + ((int64_t)at * p.splits * p.blocks + r0 / kBlock) * kPartFloats;
     const int row0 = r0 % kBlock;
     const int64_t step = (int64_t)p.blocks * kPartFloats;
-    static_assert(kMaxSplits == 16, "half a warp a row");
-    for (int r = threadIdx.x / 16; r < p.join_rows; r += 16) {
-        const int k = threadIdx.x % 16;
-        float m = -INFINITY, l = 0.0f;
-        if (k < n) {
-            const float *rec = first + k * step + row0 + r;
-            m = rec[0], l = rec[kBlock];
+    constexpr int kLanes = 16, kEach = kMaxSplits / kLanes;  // lanes of a row
+    for (int r = threadIdx.x / kLanes; r < p.join_rows; r += 256 / kLanes) {
+        const int k0 = threadIdx.x % kLanes;
+        float m[kEach], l[kEach], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int k = k0 + i * kLanes;
+            m[i] = -INFINITY, l[i] = 0.0f;
+            if (k < n) {
+                const float *rec = first + k * step + row0 + r;
+                m[i] = rec[0], l[i] = rec[kBlock];
+            }
+            top = fmaxf(top, m[i]);
         }
-        float top = m;
 #pragma unroll
-        for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float f = m > -INFINITY ? ex2(m - top) : 0.0f;
-        float sum = f * l;
+        for (int o = kLanes / 2; o; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
-        for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        weight[r][k] = f;
-        if (k > 0) continue;
+        for (int i = 0; i < kEach; ++i) {
+            const float f = m[i] > -INFINITY ? ex2(m[i] - top) : 0.0f;
+            sum += f * l[i];
+            weight[r][k0 + i * kLanes] = f;
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (k0 > 0) continue;
         inverse[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
         if (a.lse && srow0 + r < p.rows)
             a.lse[out0 + r] = (top + log2f(sum)) * 0.6931471805599453f;
@@ -1178,9 +1187,9 @@ int64_t part_bytes(const Shape &s) {
 // Whether the pages are unpacked first: what both ways cost for sequences that
 // fill their tables.  Unpacking takes 14 ns a page and head over the whole GPU,
 // and one more launch.  Measured, first against in place, 16 heads of one
-// sequence: 384 rows a head 92 against 86 us (16,512 tokens) and 34 against 32
-// (4,000); 512 rows 96 against 123 and 36 against 41; 1,000 rows 148 against
-// 224 and 54 against 62; 128 rows 62 against 41.
+// sequence: 384 rows a head 94 against 77 us (16,512 tokens) and 35 against 30
+// (4,000); 512 rows 97 against 109 and 37 against 38; 1,000 rows 149 against
+// 193 and 54 against 56; 128 rows 63 against 38.
 bool unpack_first(const Kv4Shape &k) {
     const int64_t tiles = k.n * k.max_pages * k.Hkv;
     if (tiles * kPairBytes > ((int64_t)2 << 30)) return false;

@@ -40,6 +40,22 @@ def test_few_rows_of_many_sequences(sp, n, D, dtype, Lq):
     check_attn(sp, cache, queries(n, 2, Lq, D, dtype), causal=Lq > 1)
 
 
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (64, BF16), (128, F32)])
+@pytest.mark.parametrize("lens,Hq,Hkv,Lq", [
+    ([20000], 8, 1, 1),          # one unit over every CTA
+    ([20000], 8, 1, 2),          # sixteen rows
+    ([9000, 20000, 77], 2, 1, 1),
+    ([20000, 15000], 4, 2, 3),
+    ([20000], 1, 1, 100),        # many rows: as many parts as a unit may have
+    ([9000, 20000], 2, 1, 40),
+])
+def test_few_heads_over_long_caches(sp, D, dtype, lens, Hq, Hkv, Lq):
+    cache = filled(sp, lens, Hkv, D, seed=Lq)
+    q = queries(len(lens), Hq, Lq, D, dtype)
+    for _ in range(2):  # the counters go back to zero
+        check_attn(sp, cache, q, causal=Lq > 1)
+
+
 @pytest.mark.parametrize("n,Lq", [(5, 40), (60, 20)])
 def test_lists_longer_than_their_sequences(sp, n, Lq):
     # Rows of a stride far above the blocks that any of them names.
