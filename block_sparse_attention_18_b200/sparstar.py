@@ -469,7 +469,7 @@ class Kv4Cache:
 
     def _attn_work(self, need: int, stream: int):
         """Scratch for attention calls on this stream, the current one."""
-        if torch.cuda.is_current_stream_capturing():
+        if torch._C._cuda_isCurrentStreamCapturing():
             return self._new_work(need)
         work = self._work_of.get(stream)
         if work is None or work.numel() < need:
@@ -480,6 +480,11 @@ class Kv4Cache:
         work = torch.empty(need, dtype=torch.uint8, device=self.device)
         work[:KV4_WORK_ZEROS].zero_()
         return work
+
+    def drop_work(self):
+        """Gives up the scratch of attention calls: the next calls take fresh
+        one, as they have to after a call that set STATUS_TIMEOUT."""
+        self._work_of.clear()
 
     @classmethod
     def empty(cls, n_pages: int, n_seqs: int, max_pages: int, Hkv: int, D: int, device="cuda"):
@@ -644,8 +649,9 @@ def sparstar_kv4_attn(cache: Kv4Cache, q, seqs=None, tau: float = None, causal: 
                       work=None, status=None, stream=None):
     """Attention of q [n, Hq, Lq, D] over the cached tokens of n sequences;
     returns (out, lse).  ``work`` (uint8, its first KV4_WORK_ZEROS bytes zero
-    before its first use): when not given, the cache keeps one a stream, and a
-    call that is captured into a graph gets one of its own."""
+    before its first use): when not given, the cache keeps one a stream (see
+    ``drop_work``), and a call that is captured into a graph gets one of its
+    own."""
     if _kv4_elsewhere(cache, stream):
         with _Kv4There(cache, stream):
             return sparstar_kv4_attn(cache, q, seqs, tau, causal, kv_idx, kv_cnt, out, lse,
@@ -699,9 +705,10 @@ def sparstar_kv4_attn(cache: Kv4Cache, q, seqs=None, tau: float = None, causal: 
             or not work.is_contiguous():
         raise ValueError("work must be contiguous uint8 on %s" % cache.device)
     _check(lib.sparstar_kv4_attn(
-        cache._struct, qp, dt, n, Hq, Lq, _kv4_ints(cache, seqs, "seqs", n), tau,
-        1 if causal else 0, ip, cp, max_sel if max_sel > 0 else 0, op, lp, work.data_ptr(),
-        work.numel(), _kv4_status(cache, status), s), "sparstar_kv4_attn")
+        cache._struct, qp, dt, n, Hq, Lq,
+        None if seqs is None else _kv4_ints(cache, seqs, "seqs", n), tau, 1 if causal else 0, ip,
+        cp, max_sel if max_sel > 0 else 0, op, lp, work.data_ptr(), work.numel(),
+        None if status is None else _kv4_status(cache, status), s), "sparstar_kv4_attn")
     return out, lse
 
 

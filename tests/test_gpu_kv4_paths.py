@@ -313,3 +313,15 @@ def test_page_calls_captured_into_a_graph(sp):
         # 655 + 3 * 128 tokens are more than eight pages hold.
         assert status_of(status) == ref.status == (BAD_INDEX if step == 3 else 0)
         grown.add_(128)
+
+
+def test_scratch_given_up_is_made_anew(sp):
+    cache = filled(sp, [5000], 1, 128)
+    q = queries(1, 2, 1, 128, BF16)
+    want = sp.sparstar_kv4_attn(cache, q)
+    torch.cuda.synchronize()
+    for work in cache._work_of.values():
+        work[:sp.KV4_WORK_ZEROS].fill_(1)  # as a call that gave up may leave it
+    cache.drop_work()
+    got = sp.sparstar_kv4_attn(cache, q)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
