@@ -26,6 +26,8 @@
 //     128 registers of sixteen warps.  One warp issues all products, polling
 //     for whichever is ready.
 //
+// The roles' waits are modelled in tests/test_kv4_ring_protocol.py.
+//
 // Values lie channel by channel in a page, so both operands are K-major.  Few
 // CTAs (short stripes, long caches) split the pages among several; a kernel
 // of its own joins the results, in order.
