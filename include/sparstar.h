@@ -405,7 +405,7 @@ int sparstar_transfer_lists(const int32_t *src_idx, const int32_t *src_cnt, int6
  */
 typedef struct sparstar_kv4_cache {
     void *pages;       /* [n_pages, Hkv, sparstar_kv4_page_bytes(D)], 16-byte aligned */
-    int32_t *refs;     /* [n_pages]: sequences that hold the page; 0 = free */
+    int32_t *refs;     /* [n_pages]: sequences that hold the page; 0 = free; 16-byte aligned */
     int32_t *table;    /* [n_seqs, max_pages]: page of tokens 128 j .. 128 j + 127; -1 = none */
     int32_t *lens;     /* [n_seqs]: tokens held */
     int32_t *work;     /* [sparstar_kv4_work_ints(n_pages, n_seqs)], scratch of the page calls */
