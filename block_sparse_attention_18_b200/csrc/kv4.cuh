@@ -117,7 +117,7 @@ __device__ __forceinline__ void kv4_flag(int32_t *status, int32_t bits) {
 
 // Slot of list entry i; -1 when outside the cache.
 __device__ __forceinline__ int kv4_slot(const Kv4 &c, const int32_t *seqs, int i) {
-    const int s = seqs ? __ldg(seqs + i) : i;
+    const int s = seqs ? __ldca(seqs + i) : i;
     return s >= 0 && s < c.n_seqs ? s : -1;
 }
 // Tokens of a slot, whatever the memory holds: 0 .. 128 max_pages.
@@ -130,7 +130,11 @@ __device__ __forceinline__ int kv4_len(const Kv4 &c, int slot) {
 // A cache call's kernels follow each other closely (a step resizes, writes and
 // attends), so each may be launched while the one before it still runs: its
 // CTAs take their places as that one's leave, and each waits for the whole
-// grid before it, and for that one's own wait, before it touches memory.
+// grid before it, and for that one's own wait, before it touches memory.  What
+// the calls before may have written (pages, tables and lists, but also queries
+// and tokens that came from another call) is loaded by ordinary loads behind the
+// wait: the read-only path (__ldg, const __restrict__) is defined only for
+// memory that nobody writes while the kernel is resident.
 __device__ __forceinline__ void kv4_begin() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -269,8 +269,8 @@ __device__ Tile locate(const Kv4 &c, const Kv4Attn &a, const Plan &p, const Line
     tile.block = t;
     bool listed = true;
     if (a.kv_cnt) {
-        listed = un.rows > 0 && t < __ldg(a.kv_cnt + un.list);
-        if (listed) tile.block = __ldg(a.kv_idx + un.list * a.max_sel + t);
+        listed = un.rows > 0 && t < __ldca(a.kv_cnt + un.list);
+        if (listed) tile.block = __ldca(a.kv_idx + un.list * a.max_sel + t);
     }
     if (!listed) return tile;
     if (tile.block < 0 || tile.block >= blocks) {
@@ -285,7 +285,7 @@ __device__ Tile locate(const Kv4 &c, const Kv4Attn &a, const Plan &p, const Line
     }
     if (tile.block * kBlock >= seen) return tile;
     const int slot = kv4_slot(c, a.seqs, i);
-    const int page = __ldg(c.table + (int64_t)slot * c.max_pages + tile.block);
+    const int page = __ldca(c.table + (int64_t)slot * c.max_pages + tile.block);
     if (page < 0 || page >= c.n_pages) kv4_flag(a.status, SPARSTAR_STATUS_BAD_INDEX);
     else tile.src = (int64_t)page * c.Hkv + un.kh;
     return tile;
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
                 for (int k = 0; k < KS; ++k) {
                     if constexpr (F32) {
                         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (row < un.rows) v = __ldg(reinterpret_cast<const float4 *>(src) + k);
+                        if (row < un.rows) v = __ldca(reinterpret_cast<const float4 *>(src) + k);
 #pragma unroll
                         for (int t = 0; t < kTerms; ++t) {
                             q[t][nt][k][0] = split(v.x, v.y) ^ p.flip;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
                         }
                     } else {
                         uint2 v = make_uint2(0, 0);
-                        if (row < un.rows) v = __ldg(reinterpret_cast<const uint2 *>(src) + k);
+                        if (row < un.rows) v = __ldca(reinterpret_cast<const uint2 *>(src) + k);
                         q[0][nt][k][0] = v.x ^ p.flip;
                         q[0][nt][k][1] = v.y ^ p.flip;
                     }

@@ -144,9 +144,9 @@ struct Walk {
     int n_pages;
     // The block of an entry and its page; false for one that is skipped.
     __device__ bool at(int t, int &block, int &page) const {
-        block = list ? __ldg(list + t) : t;
+        block = list ? __ldca(list + t) : t;
         if (block < 0 || block >= blocks || block >= visible) return false;
-        page = __ldg(table + block);
+        page = __ldca(table + block);
         return page >= 0 && page < n_pages;
     }
     __device__ int next(int &cur, int &page) const {
@@ -177,9 +177,9 @@ struct Stream {
             return kPages ? page : block;
         }
         if (cur >= w.hi) return 0;
-        const int block = w.list ? __ldg(w.list + cur) : cur;
+        const int block = w.list ? __ldca(w.list + cur) : cur;
         ++cur;
-        return kPages ? __ldg(w.table + block) : block;
+        return kPages ? __ldca(w.table + block) : block;
     }
     __device__ int key() {
         before = last, last = next;
@@ -228,7 +228,7 @@ __device__ Unit unit_of(const Kv4 &c, const Kv4Attn &a, const Plan &p, int unit)
         if (lists) {
             u.count[x] = 0;
             if (last >= first && u.slot >= 0) {
-                const int cnt = __ldg(a.kv_cnt + (int64_t)u.stripe * p.nqb + first / kBlock);
+                const int cnt = __ldca(a.kv_cnt + (int64_t)u.stripe * p.nqb + first / kBlock);
                 u.count[x] = cnt < 0 ? 0 : (cnt > a.max_sel ? a.max_sel : cnt);
             }
         }
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(Kv4 c, Kv4Attn a, Plan p) {
     const int block = blockIdx.x / c.Hkv % p.tile_blocks, seq = blockIdx.x / c.Hkv / p.tile_blocks;
     const int slot = kv4_slot(c, a.seqs, seq);
     if (slot < 0 || block * kBlock >= kv4_len(c, slot)) return;
-    const int page = __ldg(c.table + (int64_t)slot * c.max_pages + block);
+    const int page = __ldca(c.table + (int64_t)slot * c.max_pages + block);
     if (page < 0 || page >= c.n_pages) return;  // the attention kernel says so
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp & 3;
     const int g = lane & 3, q = lane >> 2;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(Kv4 c, Kv4Attn a, Plan p) {
     uint4 code[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        code[i] = __ldg(reinterpret_cast<const uint4 *>(half) + (32 * w + 8 * i + q) * 4 + g);
+        code[i] = __ldca(reinterpret_cast<const uint4 *>(half) + (32 * w + 8 * i + q) * 4 + g);
     extern __shared__ __align__(128) uint8_t pair[];
     uint8_t *tile = pair + (values ? kTileBytes : 0);
     auto put = [&](uint32_t at, const uint4 &v) { *reinterpret_cast<uint4 *>(tile + at) = v; };
@@ -403,13 +403,13 @@ __global__ void __launch_bounds__(256) unpack_kernel(Kv4 c, Kv4Attn a, Plan p) {
     if (values) {
         Unpack::Pairs pairs;
         const uint4 *sv = reinterpret_cast<const uint4 *>(s + w * kBlock + 32 * g);
-        u.pairs(__ldg(sv), __ldg(sv + 1), pairs);
+        u.pairs(__ldca(sv), __ldca(sv + 1), pairs);
 #pragma unroll
         for (int i = 0; i < 4; ++i) u.values(code[i], pairs, 4 * w + i, put);
     } else {
         uint32_t scale[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) scale[i] = __ldg(s + (32 * w + 8 * i + q) * 4 + g);
+        for (int i = 0; i < 4; ++i) scale[i] = __ldca(s + (32 * w + 8 * i + q) * 4 + g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) u.keys(code[i], scale[i], 4 * w + i, put);
     }
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
         int cur = wx.lo;
         for (int j = 0; j < nx; ++j) {
             int kb, page;
-            if (plain) kb = wx.list ? __ldg(wx.list + wx.lo + j) : wx.lo + j;
+            if (plain) kb = wx.list ? __ldca(wx.list + wx.lo + j) : wx.lo + j;
             else kb = wx.next(cur, page);
             if (!wait_warp(bar_s(kPre ? x : 0), (uint32_t)j & 1u, abort_flag, status)) {
                 ok = false;

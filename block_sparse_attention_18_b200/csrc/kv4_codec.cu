@@ -178,17 +178,17 @@ __device__ bool find_span(const Kv4 &c, int n, int64_t T, int per_seq, const int
     sp.i = b / c.Hkv / per_seq;
     const bool says = sp.h == 0 && j == 0 && threadIdx.x == 0;
     const int slot = kv4_slot(c, seqs, sp.i);
-    const int count = counts ? __ldg(counts + sp.i) : (int)T;
+    const int count = counts ? __ldca(counts + sp.i) : (int)T;
     bool bad = slot < 0 || count < 0 || count > T;
     int start = 0;
     if (!bad) {
         const int L = kv4_len(c, slot);
-        start = starts ? __ldg(starts + sp.i) : (write ? L - count : 0);
+        start = starts ? __ldca(starts + sp.i) : (write ? L - count : 0);
         bad = start < 0 || start > L - count;
     }
     if (write && seqs && !bad) {
         int twice = 0;
-        for (int k = threadIdx.x; k < sp.i; k += blockDim.x) twice |= __ldg(seqs + k) == slot;
+        for (int k = threadIdx.x; k < sp.i; k += blockDim.x) twice |= __ldca(seqs + k) == slot;
         bad = __syncthreads_or(twice) != 0;
     }
     if (bad) {
@@ -200,7 +200,7 @@ __device__ bool find_span(const Kv4 &c, int n, int64_t T, int per_seq, const int
     sp.t0 = sp.shift > 0 ? sp.shift : 0;
     sp.t1 = sp.shift + kBlock < count ? sp.shift + kBlock : count;
     if (sp.t0 >= sp.t1) return false;
-    sp.page = __ldg(c.table + (int64_t)slot * c.max_pages + col);
+    sp.page = __ldca(c.table + (int64_t)slot * c.max_pages + col);
     if (sp.page < 0 || sp.page >= c.n_pages) {
         if (threadIdx.x == 0) kv4_flag(status, SPARSTAR_STATUS_BAD_INDEX);
         return false;
@@ -214,9 +214,9 @@ __device__ bool find_span(const Kv4 &c, int n, int64_t T, int per_seq, const int
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-    write_kernel(Kv4 c, const T *__restrict__ k, const T *__restrict__ v, int n, int64_t tokens,
-                 int per_seq, const int32_t *__restrict__ seqs, const int32_t *__restrict__ starts,
-                 const int32_t *__restrict__ counts, int32_t *status) {
+    write_kernel(Kv4 c, const T *k, const T *v, int n, int64_t tokens, int per_seq,
+                 const int32_t *seqs, const int32_t *starts, const int32_t *counts,
+                 int32_t *status) {
     constexpr int G = D / kGroup;     // groups of a token
     constexpr int W = D / 8;          // words of eight channels of a token
     constexpr int kStride = W + 1;    // odd: the transpose reads a column of words
@@ -294,9 +294,8 @@ __device__ __forceinline__ void store8(float *p, uint32_t w, uint32_t code) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-    read_kernel(Kv4 c, T *__restrict__ k, T *__restrict__ v, int n, int64_t tokens, int per_seq,
-                const int32_t *__restrict__ seqs, const int32_t *__restrict__ starts,
-                const int32_t *__restrict__ counts, int32_t *status) {
+    read_kernel(Kv4 c, T *k, T *v, int n, int64_t tokens, int per_seq, const int32_t *seqs,
+                const int32_t *starts, const int32_t *counts, int32_t *status) {
     constexpr int G = D / kGroup, W = D / 8;
     constexpr int kStride = W + 1;
     __shared__ uint32_t words[kBlock * kStride];
@@ -323,7 +322,7 @@ __global__ void __launch_bounds__(kThreads)
             int cw, tw;
             if (!tile_of(i, cw, tw)) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[i][e] = __ldg(codes + (cw * 8 + e) * (kBlock / 8) + tw);
+            for (int e = 0; e < 8; ++e) r[i][e] = __ldca(codes + (cw * 8 + e) * (kBlock / 8) + tw);
         }
     }
     const int items = (last - first) * W;
@@ -336,8 +335,8 @@ __global__ void __launch_bounds__(kThreads)
             for (int i = 0; i < 4; ++i) {
                 const int it = it0 + i * kThreads, slot = first + it / W, w = it % W;
                 if (it >= items) continue;
-                word[i] = __ldg(codes + slot * W + w);
-                scale[i] = __ldg(scales + slot * G + w / 4);
+                word[i] = __ldca(codes + slot * W + w);
+                scale[i] = __ldca(scales + slot * G + w / 4);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -363,7 +362,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int it = it0 + i * kThreads, slot = first + it / W, w = it % W;
-                if (it < items) scale[i] = __ldg(scales + (w / 4) * kBlock + slot);
+                if (it < items) scale[i] = __ldca(scales + (w / 4) * kBlock + slot);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

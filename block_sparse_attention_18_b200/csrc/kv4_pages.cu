@@ -203,10 +203,10 @@ __device__ void plan(const Kv4 &c, const int32_t *slots, const int32_t *src, con
                     ok = e.from >= 0 && e.old_len == 0;
                     for (int k = 0; k < n && ok; ++k) ok = entries[k].slot != e.from;
                     const int have = ok ? kv4_len(c, e.from) : 0;
-                    e.new_len = lens ? __ldg(lens + i) : have;
+                    e.new_len = lens ? __ldca(lens + i) : have;
                     ok = ok && e.new_len >= 0 && e.new_len <= have;
                 } else {
-                    e.new_len = __ldg(lens + i);
+                    e.new_len = __ldca(lens + i);
                     ok = e.new_len >= 0 && e.new_len <= (int64_t)c.max_pages * kBlock;
                 }
             }
@@ -318,14 +318,14 @@ __global__ void __launch_bounds__(256)
     bool bad = s < 0 || d < 0;
     int refuse = 0;
     for (int k = threadIdx.x; k < n; k += blockDim.x) {
-        const int other = __ldg(dst + k);
+        const int other = __ldca(dst + k);
         refuse |= other == s || (k < i && other == d);
     }
     bad |= __syncthreads_or(refuse) != 0;
     int L = 0;
     if (!bad) {
         const int have = kv4_len(c, s);
-        L = len ? __ldg(len + i) : have;
+        L = len ? __ldca(len + i) : have;
         bad = L < 0 || L > have || kv4_len(c, d) != 0;
     }
     __syncthreads();  // every thread has read lens[d]
