@@ -115,14 +115,17 @@ __device__ __forceinline__ bool is_page(const Kv4 &c, int p) { return p >= 0 && 
 // Copies the listed pages, a page of one head (17 or 9 KB) at a time: a warp
 // has one stage of shared memory, brings the piece in with one bulk copy and
 // sends it off with another.  The CTA's 12 or 24 stages (209 KB) are in flight
-// at once, which a few hundred registers could not hold.
+// at once, which a few hundred registers could not hold.  False in a warp whose
+// copy did not arrive in two seconds (`withhold`: the test hook's, which brings
+// none in); it waits as long again before it leaves, so that the copy does not
+// outlive its stage.
 constexpr int kStageBytes = 12 * kv4_page_bytes(128);
 constexpr int kMaxStages = kStageBytes / kv4_page_bytes(64);
-__device__ void copy_pages(const Kv4 &c, const Work &w, int pairs, int cta, int ctas,
-                           uint64_t *bars, uint8_t *smem, int32_t *status) {
+__device__ bool copy_pages(const Kv4 &c, const Work &w, int pairs, int cta, int ctas,
+                           uint64_t *bars, uint8_t *smem, bool withhold) {
     const int bytes = kv4_page_bytes(c.D), stages = kStageBytes / bytes;
     const int warp = threadIdx.x >> 5;
-    if (warp >= stages || (threadIdx.x & 31) != 0) return;
+    if (warp >= stages || (threadIdx.x & 31) != 0) return true;
     uint64_t *mbar = bars + warp;
     const uint32_t bar = (uint32_t)__cvta_generic_to_shared(mbar);
     const uint32_t stage = (uint32_t)__cvta_generic_to_shared(smem + warp * bytes);
@@ -136,14 +139,16 @@ __device__ void copy_pages(const Kv4 &c, const Work &w, int pairs, int cta, int 
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
                      "r"(bytes)
                      : "memory");
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-            "[%3];" ::"r"(stage),
-            "l"(c.pages + ((int64_t)from * c.Hkv + h) * bytes), "r"(bytes), "r"(bar)
-            : "memory");
+        if (!withhold)
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+                "[%3];" ::"r"(stage),
+                "l"(c.pages + ((int64_t)from * c.Hkv + h) * bytes), "r"(bytes), "r"(bar)
+                : "memory");
         if (!kv4_wait(bar, phase)) {
-            kv4_flag(status, SPARSTAR_STATUS_TIMEOUT);
-            break;
+            kv4_wait(bar, phase);
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            return false;
         }
         phase ^= 1u;
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
@@ -154,6 +159,7 @@ __device__ void copy_pages(const Kv4 &c, const Work &w, int pairs, int cta, int 
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    return true;
 }
 
 // resize (src NULL: slots, lens) and deep fork (src, slots = dst, lens).
@@ -379,19 +385,22 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Kv4 c, int32
     }
 }
 
-// Copies the listed pages; with `remap`, also renames the moved ones in the
-// tables.
+// Copies the listed pages; for a compaction (n_live given) also renames the
+// moved ones in the tables.  A copy that gave up is said in *status and *n_live.
 constexpr int kCopyThreads = 32 * kMaxStages;
 __global__ void __launch_bounds__(kCopyThreads)
-    copy_kernel(Kv4 c, bool remap, int32_t *status) {
+    copy_kernel(Kv4 c, int32_t *n_live, int32_t *status, bool withhold) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[kMaxStages];
     kv4_begin();
     const Work w = work_of(c);
     const int pairs = w.pairs[0];
     if (pairs == 0) return;
-    copy_pages(c, w, pairs, blockIdx.x, gridDim.x, bars, smem, status);
-    if (!remap) return;
+    if (!copy_pages(c, w, pairs, blockIdx.x, gridDim.x, bars, smem, withhold)) {
+        kv4_flag(status, SPARSTAR_STATUS_TIMEOUT);
+        if (n_live) atomicExch(n_live, -1);
+    }
+    if (!n_live) return;
     const int live = w.pairs[1];
     const int64_t entries = (int64_t)c.n_seqs * c.max_pages;
     for (int64_t e = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; e < entries;
@@ -403,11 +412,13 @@ __global__ void __launch_bounds__(kCopyThreads)
     }
 }
 
-cudaError_t launch_copy(const Kv4 &c, bool remap, int32_t *status, cudaStream_t stream) {
+cudaError_t launch_copy(const Kv4 &c, int32_t *n_live, int32_t *status, bool withhold,
+                        cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(
         copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes);
     if (e != cudaSuccess) return e;
-    return launch_after(copy_kernel, 148, kCopyThreads, kStageBytes, stream, c, remap, status);
+    return launch_after(copy_kernel, 148, kCopyThreads, kStageBytes, stream, c, n_live, status,
+                        withhold);
 }
 
 }  // namespace
@@ -433,14 +444,15 @@ cudaError_t launch_kv4_fork(const Kv4 &c, const int32_t *src, const int32_t *dst
     const cudaError_t e =
         launch_after(plan_kernel, 1, kPlanThreads, 0, stream, c, dst, src, len, n, status);
     if (e != cudaSuccess) return e;
-    return launch_copy(c, false, status, stream);
+    return launch_copy(c, nullptr, status, false, stream);
 }
 
-cudaError_t launch_kv4_compact(const Kv4 &c, int32_t *n_live, cudaStream_t stream) {
+cudaError_t launch_kv4_compact(const Kv4 &c, int32_t *n_live, cudaStream_t stream,
+                               bool withhold) {
     const cudaError_t e =
         launch_after(compact_plan_kernel, 1, kPlanThreads, 0, stream, c, n_live);
     if (e != cudaSuccess) return e;
-    return launch_copy(c, true, nullptr, stream);
+    return launch_copy(c, n_live, nullptr, withhold, stream);
 }
 
 }  // namespace sparstar

@@ -421,15 +421,29 @@ SPARSTAR_API int sparstar_kv4_fork(const sparstar_kv4_cache *cache, const int32_
                                                  static_cast<cudaStream_t>(stream)));
 }
 
-SPARSTAR_API int sparstar_kv4_compact(const sparstar_kv4_cache *cache, int32_t *n_live,
-                                      void *stream) {
-    TraceRange trace("sparstar_kv4_compact");
+namespace {
+
+int kv4_compact(const sparstar_kv4_cache *cache, int32_t *n_live, void *stream, bool withhold) {
     sparstar::Kv4 c;
     if (int rc = kv4_cache_check(cache, true, &c)) return rc;
     if (!n_live || !aligned4(n_live)) return SPARSTAR_EINVAL;
     if (int rc = device_check()) return rc;
     return cuda_status(
-        sparstar::launch_kv4_compact(c, n_live, static_cast<cudaStream_t>(stream)));
+        sparstar::launch_kv4_compact(c, n_live, static_cast<cudaStream_t>(stream), withhold));
+}
+
+}  // namespace
+
+SPARSTAR_API int sparstar_kv4_compact(const sparstar_kv4_cache *cache, int32_t *n_live,
+                                      void *stream) {
+    TraceRange trace("sparstar_kv4_compact");
+    return kv4_compact(cache, n_live, stream, false);
+}
+
+SPARSTAR_API int sparstar_test_kv4_compact_timeout(const sparstar_kv4_cache *cache,
+                                                   int32_t *n_live, void *stream) {
+    TraceRange trace("sparstar_test_kv4_compact_timeout");
+    return kv4_compact(cache, n_live, stream, true);
 }
 
 SPARSTAR_API int sparstar_kv4_write(const sparstar_kv4_cache *cache, const void *k,

@@ -104,7 +104,9 @@ cudaError_t launch_kv4_resize(const Kv4 &c, const int32_t *seqs, const int32_t *
 cudaError_t launch_kv4_fork(const Kv4 &c, const int32_t *src, const int32_t *dst,
                             const int32_t *len, int n, bool deep, int32_t *status,
                             cudaStream_t stream);
-cudaError_t launch_kv4_compact(const Kv4 &c, int32_t *n_live, cudaStream_t stream);
+// withhold: a test hook that brings no page in, so that the copies give up.
+cudaError_t launch_kv4_compact(const Kv4 &c, int32_t *n_live, cudaStream_t stream,
+                               bool withhold = false);
 cudaError_t launch_kv4_write(const Kv4 &c, const void *k, const void *v, int dtype, int n,
                              int64_t T, const int32_t *seqs, const int32_t *starts,
                              const int32_t *counts, int32_t *status, cudaStream_t stream);

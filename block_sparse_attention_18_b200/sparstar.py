@@ -79,6 +79,8 @@ def _load():
     L.sparstar_kv4_resize.argtypes = [kv4, vp, vp, i64, vp, vp]
     L.sparstar_kv4_fork.argtypes = [kv4, vp, vp, vp, i64, i32, vp, vp]
     L.sparstar_kv4_compact.argtypes = [kv4, vp, vp]
+    L.sparstar_test_kv4_compact_timeout.argtypes = [kv4, vp, vp]
+    L.sparstar_test_kv4_compact_timeout.restype = i32
     L.sparstar_kv4_write.argtypes = [kv4, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp]
     L.sparstar_kv4_read.argtypes = [kv4, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp]
     L.sparstar_kv4_attn.argtypes = [kv4, vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, i64, vp,
@@ -572,7 +574,8 @@ def sparstar_kv4_fork(cache: Kv4Cache, src, dst, lens=None, deep: bool = False, 
 
 
 def sparstar_kv4_compact(cache: Kv4Cache, n_live=None, stream=None):
-    """Moves the live pages to the lowest places; returns their number (device)."""
+    """Moves the live pages to the lowest places; returns their number (device),
+    or -1 there when the copy of a page gave up: fill the cache anew."""
     if _kv4_elsewhere(cache, stream):
         with _Kv4There(cache, stream):
             return sparstar_kv4_compact(cache, n_live)
@@ -726,3 +729,11 @@ def sparstar_test_attn_timeout(q, k, v, kv_idx, kv_cnt, out, status, stream=None
                                           _ptr(kv_idx), _ptr(kv_cnt), kv_idx.shape[-1],
                                           _ptr(out), _ptr(status), _stream(stream)),
            "sparstar_test_attn_timeout")
+
+
+def sparstar_test_kv4_compact_timeout(cache: Kv4Cache, n_live):
+    """Test hook: a compaction with its copies withheld, so that they give up
+    and n_live (an int32 device tensor) becomes -1."""
+    _check(lib.sparstar_test_kv4_compact_timeout(
+        cache._struct, _kv4_tensor(cache, n_live, "n_live", torch.int32, (1,)),
+        _kv4_raw_stream(cache)), "sparstar_test_kv4_compact_timeout")

@@ -458,7 +458,9 @@ int sparstar_kv4_fork(const sparstar_kv4_cache *cache, const int32_t *src, const
  * sparstar_kv4_compact — moves pages so that the n live ones are pages
  * 0..n-1, and writes n to *n_live (device).  The k-th lowest live page at or
  * above n moves to the k-th lowest free page below n; pages behind the live
- * ones keep their bytes.
+ * ones keep their bytes.  *n_live = -1 says that the copy of a page gave up
+ * after two seconds (as SPARSTAR_STATUS_TIMEOUT does elsewhere): the tables then
+ * name pages that were not copied, and the cache has to be filled anew.
  */
 int sparstar_kv4_compact(const sparstar_kv4_cache *cache, int32_t *n_live, void *stream);
 
@@ -538,6 +540,14 @@ int sparstar_test_attn_timeout(const void *q, const void *k, const void *v, int6
                                int64_t Lq, int64_t Lk, const int32_t *kv_idx,
                                const int32_t *kv_cnt, int64_t max_sel, void *out,
                                int32_t *status, void *stream);
+
+/*
+ * sparstar_test_kv4_compact_timeout — TEST HOOK for failure detection:
+ * sparstar_kv4_compact with the copies of pages withheld, so that each waits
+ * until it gives up (about four seconds in all) and *n_live becomes -1.
+ */
+int sparstar_test_kv4_compact_timeout(const sparstar_kv4_cache *cache, int32_t *n_live,
+                                      void *stream);
 
 /* Message for a status code (static storage). */
 const char *sparstar_strerror(int code);
