@@ -63,8 +63,9 @@ struct Plan {
     int units;       // units of a sequence
     int row_tiles;   // units of a stripe
     int nqb;         // query blocks of a head (lists)
-    float sc;        // |tau| in log2 units
+    float sc;        // |tau| in log2 units; 1 for tau = 0
     uint32_t flip;   // sign bits to flip in q (tau < 0)
+    bool flat;       // tau = 0: q is multiplied by 0
     uint32_t *arrived;  // [kCtas]: high half: CTAs (or groups) whose partial result of the
                         // unit that begins in this CTA and goes on is stored; low half:
                         // CTAs of the group that begins here; 0 between calls
@@ -143,6 +144,10 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return as_u32(__floats2bfloat162_rn(lo, hi));
+}
+// A bf16 pair times 0: infinities and NaN give NaN.
+__device__ __forceinline__ uint32_t times0(uint32_t x) {
+    return as_u32(__hmul2(as_bf162(x), __float2bfloat162_rn(0.0f)));
 }
 // Takes the bf16 part of two fp32 values off them.
 __device__ __forceinline__ uint32_t split(float &lo, float &hi) {
@@ -560,6 +565,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
                     if constexpr (F32) {
                         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (row < un.rows) v = __ldca(reinterpret_cast<const float4 *>(src) + k);
+                        if (p.flat) v.x *= 0.0f, v.y *= 0.0f, v.z *= 0.0f, v.w *= 0.0f;
 #pragma unroll
                         for (int t = 0; t < kTerms; ++t) {
                             q[t][nt][k][0] = split(v.x, v.y) ^ p.flip;
@@ -568,6 +574,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
                     } else {
                         uint2 v = make_uint2(0, 0);
                         if (row < un.rows) v = __ldca(reinterpret_cast<const uint2 *>(src) + k);
+                        if (p.flat) v.x = times0(v.x), v.y = times0(v.y);
                         q[0][nt][k][0] = v.x ^ p.flip;
                         q[0][nt][k][1] = v.y ^ p.flip;
                     }
@@ -1076,9 +1083,10 @@ cudaError_t launch_kv4_attn_few(const Kv4 &c, const Kv4Attn &a, int dtype, cudaS
     p.row_tiles = (rows + R - 1) / R;
     p.nqb = (a.Lq + kBlock - 1) / kBlock;
     p.units = p.row_tiles * (lists ? a.Hq * p.nqb : c.Hkv);
-    // A scale of 0 would turn masked scores (-inf) into NaN; this one leaves
-    // every score below 2^-90.
-    p.sc = fmaxf(fabsf(a.tau) * 1.4426950408889634f, 1e-37f);
+    // A scale of 0 would turn masked scores (-inf) into NaN: it goes into the
+    // queries instead.  No other tau has a product of 0.
+    p.flat = a.tau == 0.0f;
+    p.sc = p.flat ? 1.0f : fabsf(a.tau) * 1.4426950408889634f;
     p.flip = a.tau < 0.0f ? 0x80008000u : 0u;
     p.arrived = static_cast<uint32_t *>(a.work);
     p.joins = static_cast<float *>(a.work) + kArrivedBytes / 4;
