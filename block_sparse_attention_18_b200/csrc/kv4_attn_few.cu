@@ -7,9 +7,9 @@
 // a stripe.  Its work is one tile a page.
 //
 // Split.  All units' tiles form one line, cut into equal parts for 148 CTAs
-// and again for the parts of a CTA, a warp or a pair of warps each: lengths
-// from 1 to 144,512 tokens in one batch keep every warp equally busy, and one
-// long sequence is spread over the whole GPU.  A part may begin and end inside
+// and again for the parts of a CTA, a warp each, or a pair of warps on one tile:
+// lengths from 1 to 144,512 tokens in one batch keep every warp equally busy, and
+// one long sequence is spread over the whole GPU.  A part may begin and end inside
 // a unit; such partial results (running maximum, sum, accumulator) are joined
 // inside the CTA in shared memory, and across CTAs by the last one to arrive
 // (in groups first, where they are many), always in the order of the line, so
@@ -71,7 +71,7 @@ struct Plan {
                         // CTAs of the group that begins here; 0 between calls
     float *joins;       // [kCtas][2][R][D + 2]: a CTA's partial results: of the unit that
                         // goes on from the CTA before, of the one that begins here
-    float *ends;        // [kCtas * kParts][kPair][R][D + 2]: ends of units inside a part
+    float *ends;        // [kCtas * kParts][R][D + 2]: ends of units inside a part
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
@@ -85,9 +85,6 @@ __device__ __forceinline__ uint64_t globaltimer() {
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
                  : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -404,10 +401,12 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     constexpr int kRow = D + 4;                // joined rows: conflict-free stores
     using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
     static_assert(kThreads >= kChunks, "build_line: one chunk a thread");
-    static_assert(kParts * kPair * R <= kEndRows, "scratch");
+    static_assert(kParts * R <= kEndRows, "scratch");
+    // A pair has one tile (launch_kv4_attn_few), a half of it each warp: all it
+    // copies is in the ring at once, and its results stay in registers.
+    static_assert(kPair == 1 || kStages >= 2, "a tile's keys and values");
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t full[kParts][kStages], empty[kParts][kStages];
-    __shared__ uint64_t given[kParts], taken[kParts];  // the pair's exchange
+    __shared__ uint64_t full[kParts][kStages];
     __shared__ int64_t prefix[kChunks + 1], sums[kParts * kPair];
     // Partial results of the parts, in the order of the line: the end of a
     // unit inside part k (2 k), what the part's end leaves (2 k + 1).
@@ -422,12 +421,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     const int r = lane >> 2, j = lane & 3;
     const bool leads = member == 0;
     if (lane == 0 && leads) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[part][s], 1);
-            mbar_init(&empty[part][s], kPair);
-        }
-        mbar_init(&given[part], 1);
-        mbar_init(&taken[part], 1);
+        for (int s = 0; s < kStages; ++s) mbar_init(&full[part][s], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     kv4_begin();
@@ -491,9 +485,6 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         if (todo == 0) return;
         const int at = __ffsll((long long)todo) - 1;
         const int s = issued % kStages;
-        // Both warps of a pair have read what the stage held.
-        if (kPair > 1 && leads && issued >= kStages)
-            ok = ok && wait_warp(&empty[part][s], (issued / kStages - 1) & 1u);
         if (leads && lane == (at & 31) && ok)
             bulk_load(smem_u32(ring + s * kHalf),
                       c.pages + (at < 32 ? now.src : next.src) * (2 * kHalf) + half_of * kHalf,
@@ -505,7 +496,6 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     for (int s = 0; s < kStages; ++s) issue();
     auto release = [&]() {  // the oldest half is read; refill its stage
         __syncwarp();
-        if (kPair > 1 && lane == 0) mbar_arrive(&empty[part][used % kStages]);
         ++used;
         issue();
     };
@@ -516,7 +506,6 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     int seen[NT][2];                // tokens that rows 2 j, 2 j + 1 see
     int seen_min = 0;
     int uid = -1, started = 0;      // unit at work; it began with its first tile
-    uint32_t joined = 0;            // exchanges of the pair
     if (lane == 0 && leads) entry[2 * part] = entry[2 * part + 1] = -1;
 
     // Sums over the lanes that share rows.
@@ -791,83 +780,17 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         }
         ++x;
         const bool ends = (t_edge & 2) != 0;
-        if (x < x1 && !ends) continue;
+        if (kPair == 1 && x < x1 && !ends) continue;
         // The unit ends here, or the part does.
         reduce_l();
-        if (x == x1) {  // what the part's end leaves stays in registers
+        if (kPair > 1 || x == x1) {  // what the part's end leaves stays in registers
             if (lane == 0 && leads) {
                 entry[2 * part + 1] = uid;
                 edges[2 * part + 1] = started | (t_edge & 2);
             }
             break;
         }
-        if (kPair > 1 && started) {
-            // The pair's results join in the leading warp, a quarter of the
-            // accumulator at a time.
-            float4 *box = reinterpret_cast<float4 *>(smem + kParts * kStages * kHalf) +
-                          part * (KS / 4 + 1) * NT * 32 + lane;
-            float fa[NT][2], fb[NT][2];
-#pragma unroll
-            for (int qt = 0; qt < 4 && ok; ++qt) {
-                if (!leads) {
-                    if (joined) ok = wait_warp(&taken[part], (joined - 1) & 1u);
-                    if (!ok) break;
-                    if (qt == 0) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            box[(KS / 4 * NT + nt) * 32] =
-                                make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < KS / 4; ++k)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const float(&v)[4] = o[qt * KS / 4 + k][nt];
-                            box[(k * NT + nt) * 32] = make_float4(v[0], v[1], v[2], v[3]);
-                        }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&given[part]);
-                } else {
-                    ok = wait_warp(&given[part], joined & 1u);
-                    if (!ok) break;
-                    if (qt == 0) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const float4 b = box[(KS / 4 * NT + nt) * 32];
-                            const float mb[2] = {b.x, b.y}, lb[2] = {b.z, b.w};
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float top = fmaxf(m[nt][e], mb[e]);
-                                fa[nt][e] = m[nt][e] > -INFINITY ? ex2(m[nt][e] - top) : 0.0f;
-                                fb[nt][e] = mb[e] > -INFINITY ? ex2(mb[e] - top) : 0.0f;
-                                l[nt][e] = l[nt][e] * fa[nt][e] + lb[e] * fb[nt][e];
-                                m[nt][e] = top;
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < KS / 4; ++k)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float(&v)[4] = o[qt * KS / 4 + k][nt];
-                            const float4 b = box[(k * NT + nt) * 32];
-                            v[0] = v[0] * fa[nt][0] + b.x * fb[nt][0];
-                            v[1] = v[1] * fa[nt][1] + b.y * fb[nt][1];
-                            v[2] = v[2] * fa[nt][0] + b.z * fb[nt][0];
-                            v[3] = v[3] * fa[nt][1] + b.w * fb[nt][1];
-                        }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&taken[part]);
-                }
-                ++joined;
-            }
-            if (!ok) break;
-        }
         if (started) {  // whole: straight to the output
-            if (!leads) {
-                uid = -1;
-                continue;
-            }
             const Unit un = unit_of<R>(c, a, p, uid);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -887,7 +810,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
                             (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
                 }
         } else {  // the end of a unit that began before this part
-            float *rec = p.ends + (int64_t)(slot_id * kPair + member) * R * (D + 2);
+            float *rec = p.ends + (int64_t)slot_id * R * (D + 2);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -903,7 +826,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
                         rec[R * D + R + row] = l[nt][e];
                     }
                 }
-            if (lane == 0 && leads) {
+            if (lane == 0) {
                 entry[2 * part] = uid;
                 edges[2 * part] = 2;
             }
@@ -918,7 +841,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     // ------------------------------ the parts' partial results, unit by unit
     __syncthreads();
     constexpr int kRecord = R * (D + 2);
-    constexpr int kWarps = kParts * kPair, kHeld = 2 * kWarps;
+    constexpr int kWarps = kParts * kPair, kHeld = kWarps + (kPair == 1 ? kParts : 0);
     // What each warp's registers hold, then the ends inside parts: [kHeld].
     float *so = reinterpret_cast<float *>(smem);  // [kHeld][R][kRow]
     float *sm = so + kHeld * R * kRow, *sl = sm + kHeld * R;
@@ -974,9 +897,9 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
                 }
             }
     }
-    if (entry[2 * part] >= 0) {
-        const float *rec = p.ends + (int64_t)(slot_id * kPair + member) * kRecord;
-        const int w = kWarps + part * kPair + member;
+    if (kPair == 1 && entry[2 * part] >= 0) {
+        const float *rec = p.ends + (int64_t)slot_id * kRecord;
+        const int w = kWarps + part;
         for (int v = lane; v < R * D / 4; v += 32)
             *reinterpret_cast<float4 *>(so + (w * R + v / (D / 4)) * kRow + v % (D / 4) * 4) =
                 *reinterpret_cast<const float4 *>(rec + 4 * v);
@@ -1050,9 +973,9 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
 template <int D, int NT, bool F32, int kParts, int kPair>
 cudaError_t launch(const Kv4 &c, const Kv4Attn &a, const Plan &p, cudaStream_t stream) {
     constexpr int kStages = 24 * (128 / D) / kParts;  // 209 KB
-    constexpr int kBox = kPair > 1 ? kParts * (D / 64 + 1) * NT * 32 * 16 : 0;
-    constexpr int kRing = kParts * kStages * kv4_half_bytes(D) + kBox;
-    constexpr int kJoin = 2 * kParts * kPair * 8 * NT * (D + 4 + 2) * 4;
+    constexpr int kRing = kParts * kStages * kv4_half_bytes(D);
+    constexpr int kHeld = kParts * kPair + (kPair == 1 ? kParts : 0);
+    constexpr int kJoin = kHeld * 8 * NT * (D + 4 + 2) * 4;
     constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
     const auto kernel = few_kernel<D, NT, F32, kParts, kPair, kStages>;
     cudaError_t e =
@@ -1098,16 +1021,18 @@ cudaError_t launch_kv4_attn_few(const Kv4 &c, const Kv4Attn &a, int dtype, cudaS
     // against 18.9; below, 1,000 tokens, 12.0 against 11.3, and above, 15,000
     // tokens, 23.8 against 22.6).
     const double most = (double)a.n * p.units * (lists ? a.max_sel : c.max_pages);
-    const bool pairs = most > 2.0 * kCtas && most <= 8.0 * kCtas;
+    // Not more than 8 * 148 tiles: no part of 8 * 148 has more than one.
+    constexpr int kPairs = 8;
+    const bool pairs = most > 2.0 * kCtas && most <= (double)kPairs * kCtas;
     if (c.D == 128) {
         if (f32) return launch<128, 1, true, 8, 1>(c, a, p, stream);
         if (R == 16) return launch<128, 2, false, 8, 1>(c, a, p, stream);
-        return pairs ? launch<128, 1, false, 8, 2>(c, a, p, stream)
+        return pairs ? launch<128, 1, false, kPairs, 2>(c, a, p, stream)
                      : launch<128, 1, false, 12, 1>(c, a, p, stream);
     }
     if (f32) return launch<64, 1, true, 8, 1>(c, a, p, stream);
     if (R == 16) return launch<64, 2, false, 8, 1>(c, a, p, stream);
-    return pairs ? launch<64, 1, false, 8, 2>(c, a, p, stream)
+    return pairs ? launch<64, 1, false, kPairs, 2>(c, a, p, stream)
                  : launch<64, 1, false, 12, 1>(c, a, p, stream);
 }
 
