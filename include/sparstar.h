@@ -434,10 +434,12 @@ int64_t sparstar_kv4_work_ints(int64_t n_pages, int64_t n_seqs);
  *   new_lens [n] int32 (device), 0 .. 128 max_pages; 0 frees the sequence
  * Growing takes free pages, the lowest first, in the order of the list; when
  * the last page is partial and shared, the sequence first gets its own copy
- * of it.  If the free pages at the start of the call do not suffice for the
- * entries up to and including one, that entry keeps its length and sets
- * SPARSTAR_STATUS_NO_PAGES.  Shrinking gives pages up; they are free for the
- * next call.  The new tokens are undefined until they are written.
+ * of it.  An entry that needs pages, where the free pages at the start of the
+ * call do not suffice for what the entries up to and including it need, keeps
+ * its length and sets SPARSTAR_STATUS_NO_PAGES.  One that needs none (it
+ * shrinks, or grows within a page of its own) is served whatever the entries
+ * before it needed.  Shrinking gives pages up; they are free for the next call.
+ * The new tokens are undefined until they are written.
  */
 int sparstar_kv4_resize(const sparstar_kv4_cache *cache, const int32_t *seqs,
                         const int32_t *new_lens, int64_t n, int32_t *status, void *stream);
