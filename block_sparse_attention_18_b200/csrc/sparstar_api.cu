@@ -374,9 +374,11 @@ int kv4_cache_check(const sparstar_kv4_cache *cache, bool uses_work, sparstar::K
 }
 
 int kv4_token_check(int64_t n, int64_t T, const sparstar::Kv4 &c, const void *k, const void *v,
-                    const void *starts, const void *counts) {
+                    const void *seqs, const void *starts, const void *counts,
+                    const void *status) {
     if (n < 1 || n > c.n_seqs || T < 1 || T > kMaxTokens) return SPARSTAR_EINVAL;
-    if (!aligned16(k) || !aligned16(v) || !aligned4(starts) || !aligned4(counts))
+    if (!aligned16(k) || !aligned16(v) || !aligned4(seqs) || !aligned4(starts) ||
+        !aligned4(counts) || !aligned4(status))
         return SPARSTAR_EINVAL;
     // one CTA a touched page of every sequence and head
     if (n * (ceil_div(T, kBlock) + 1) > kMaxGrid / c.Hkv) return SPARSTAR_EINVAL;
@@ -400,7 +402,8 @@ SPARSTAR_API int sparstar_kv4_resize(const sparstar_kv4_cache *cache, const int3
     TraceRange trace("sparstar_kv4_resize");
     sparstar::Kv4 c;
     if (int rc = kv4_cache_check(cache, true, &c)) return rc;
-    if (!new_lens || n < 1 || n > c.n_seqs || !aligned4(seqs) || !aligned4(new_lens))
+    if (!new_lens || n < 1 || n > c.n_seqs || !aligned4(seqs) || !aligned4(new_lens) ||
+        !aligned4(status))
         return SPARSTAR_EINVAL;
     if (int rc = device_check()) return rc;
     return cuda_status(sparstar::launch_kv4_resize(c, seqs, new_lens, (int)n, status,
@@ -414,7 +417,7 @@ SPARSTAR_API int sparstar_kv4_fork(const sparstar_kv4_cache *cache, const int32_
     sparstar::Kv4 c;
     if (int rc = kv4_cache_check(cache, true, &c)) return rc;
     if (!src || !dst || n < 1 || n > c.n_seqs || (deep != 0 && deep != 1) || !aligned4(src) ||
-        !aligned4(dst) || !aligned4(len))
+        !aligned4(dst) || !aligned4(len) || !aligned4(status))
         return SPARSTAR_EINVAL;
     if (int rc = device_check()) return rc;
     return cuda_status(sparstar::launch_kv4_fork(c, src, dst, len, (int)n, deep != 0, status,
@@ -455,7 +458,7 @@ SPARSTAR_API int sparstar_kv4_write(const sparstar_kv4_cache *cache, const void 
     if (!dtype_ok(dtype)) return SPARSTAR_EDTYPE;
     if (int rc = kv4_cache_check(cache, false, &c)) return rc;
     if (!k || !v) return SPARSTAR_EINVAL;
-    if (int rc = kv4_token_check(n, T, c, k, v, starts, counts)) return rc;
+    if (int rc = kv4_token_check(n, T, c, k, v, seqs, starts, counts, status)) return rc;
     if (int rc = device_check()) return rc;
     return cuda_status(sparstar::launch_kv4_write(c, k, v, dtype, (int)n, T, seqs, starts,
                                                   counts, status,
@@ -471,7 +474,7 @@ SPARSTAR_API int sparstar_kv4_read(const sparstar_kv4_cache *cache, void *k, voi
     if (!dtype_ok(dtype)) return SPARSTAR_EDTYPE;
     if (int rc = kv4_cache_check(cache, false, &c)) return rc;
     if (!k && !v) return SPARSTAR_EINVAL;
-    if (int rc = kv4_token_check(n, T, c, k, v, starts, counts)) return rc;
+    if (int rc = kv4_token_check(n, T, c, k, v, seqs, starts, counts, status)) return rc;
     if (int rc = device_check()) return rc;
     return cuda_status(sparstar::launch_kv4_read(c, k, v, dtype, (int)n, T, seqs, starts, counts,
                                                  status, static_cast<cudaStream_t>(stream)));
@@ -516,7 +519,7 @@ SPARSTAR_API int sparstar_kv4_attn(const sparstar_kv4_cache *cache, const void *
         (kv_idx && !kv_cnt))
         return SPARSTAR_EINVAL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(work) || !aligned4(seqs) ||
-        !aligned4(kv_idx) || !aligned4(kv_cnt) || !aligned4(lse))
+        !aligned4(kv_idx) || !aligned4(kv_cnt) || !aligned4(lse) || !aligned4(status))
         return SPARSTAR_EINVAL;
     // One list entry names one of n_seqs slots, or several entries the same.
     sparstar::Kv4Shape s;

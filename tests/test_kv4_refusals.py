@@ -1,0 +1,32 @@
+"""Refusals of the 4-bit cache's calls that test_kv4_cpu.py does not make, on a
+host without a GPU: every call below is refused before anything is launched."""
+import types
+
+import pytest
+
+from test_kv4_cpu import A, MIS, cache, sp  # noqa: F401
+
+
+def test_misaligned_lists_of_slots_are_refused(sp):
+    L, c = sp.lib, cache(sp)
+    assert L.sparstar_kv4_write(c, A, A, 0, 1, 1, MIS, 0, 0, 0, 0) == sp.EINVAL
+    assert L.sparstar_kv4_read(c, A, A, 0, 1, 1, MIS, 0, 0, 0, 0) == sp.EINVAL
+
+
+def test_misaligned_status_words_are_refused(sp):
+    L, c = sp.lib, cache(sp)
+    assert L.sparstar_kv4_resize(c, 0, A, 1, MIS, 0) == sp.EINVAL
+    assert L.sparstar_kv4_fork(c, A, A, 0, 1, 0, MIS, 0) == sp.EINVAL
+    assert L.sparstar_kv4_write(c, A, A, 0, 1, 1, 0, 0, 0, MIS, 0) == sp.EINVAL
+    assert L.sparstar_kv4_read(c, A, A, 0, 1, 1, 0, 0, 0, MIS, 0) == sp.EINVAL
+    assert L.sparstar_kv4_attn(c, A, 0, 1, 4, 1, 0, 0.1, 0, 0, 0, 0, A, 0, A, 1 << 40, MIS,
+                               0) == sp.EINVAL
+
+
+def test_the_compaction_hook_refuses_as_the_call_does(sp):
+    L = sp.lib
+    for call in (L.sparstar_kv4_compact, L.sparstar_test_kv4_compact_timeout):
+        assert call(cache(sp), 0, 0) == sp.EINVAL
+        assert call(cache(sp), MIS, 0) == sp.EINVAL
+        assert call(cache(sp, work=0), A, 0) == sp.EINVAL
+        assert call(None, A, 0) == sp.EINVAL
