@@ -524,6 +524,8 @@ def _kv4_status(cache, status):
 
 def _kv4_elsewhere(cache, stream):
     """Whether a call has to switch to the cache's device or another stream."""
+    if stream is not None and stream.device_index != cache.index:
+        raise ValueError("stream must be one of %s" % (cache.device,))
     return stream is not None or torch._C._cuda_getDevice() != cache.index
 
 

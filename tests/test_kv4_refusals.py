@@ -30,3 +30,18 @@ def test_the_compaction_hook_refuses_as_the_call_does(sp):
         assert call(cache(sp), MIS, 0) == sp.EINVAL
         assert call(cache(sp, work=0), A, 0) == sp.EINVAL
         assert call(None, A, 0) == sp.EINVAL
+
+
+def test_a_stream_of_another_device_is_refused(sp):
+    # The switch would go to that stream's device and from there back to the
+    # cache's, on whatever stream is current there.
+    here = types.SimpleNamespace(index=0, device="cuda:0")
+    there = types.SimpleNamespace(device_index=1, cuda_stream=7)
+    for call in (lambda: sp.sparstar_kv4_resize(here, None, stream=there),
+                 lambda: sp.sparstar_kv4_fork(here, None, None, stream=there),
+                 lambda: sp.sparstar_kv4_compact(here, stream=there),
+                 lambda: sp.sparstar_kv4_write(here, None, None, stream=there),
+                 lambda: sp.sparstar_kv4_read(here, 1, stream=there),
+                 lambda: sp.sparstar_kv4_attn(here, None, stream=there)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
