@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
     const int part = (threadIdx.x >> 5) / kPair, member = (threadIdx.x >> 5) % kPair;
     const int lane = threadIdx.x & 31;
     const int r = lane >> 2, j = lane & 3;
-    const bool leads = member == 0;
+    const bool leads = member == 0, copies = leads && !a.withhold;
     if (lane == 0 && leads) {
         for (int s = 0; s < kStages; ++s) mbar_init(&full[part][s], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(32 * kParts * kPair, 1) few_kernel(Kv4 c, Kv4A
         if (todo == 0) return;
         const int at = __ffsll((long long)todo) - 1;
         const int s = issued % kStages;
-        if (leads && lane == (at & 31) && ok)
+        if (copies && lane == (at & 31) && ok)
             bulk_load(smem_u32(ring + s * kHalf),
                       c.pages + (at < 32 ? now.src : next.src) * (2 * kHalf) + half_of * kHalf,
                       kHalf, &full[part][s]);

@@ -615,11 +615,12 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 if (!ok) return;
                 mbar_expect_tx(bar_full(e), kTileBytes);
                 const uint8_t *src = tiles + (int64_t)block * kPairBytes + is_v * kTileBytes;
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
-                    "[%1], %2, [%3];" ::"r"(base + kOffStage + stage * kTileBytes),
-                    "l"(src), "r"(kTileBytes), "r"(bar_full(e))
-                    : "memory");
+                if (!a.withhold)
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+                        "[%1], %2, [%3];" ::"r"(base + kOffStage + stage * kTileBytes),
+                        "l"(src), "r"(kTileBytes), "r"(bar_full(e))
+                        : "memory");
                 ++e;
             };
             if (sA > 0) load(A.key(), 0);
@@ -696,11 +697,12 @@ __global__ void __launch_bounds__(kThreads<kPre>, 1)
                 mbar_expect_tx(bar_packed(s), kHalf);
                 const uint8_t *src =
                     c.pages + ((int64_t)page * c.Hkv + kh) * (2 * kHalf) + is_v * kHalf;
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
-                    "[%1], %2, [%3];" ::"r"(base + kOffPacked + s * kHalf),
-                    "l"(src), "r"(kHalf), "r"(bar_packed(s))
-                    : "memory");
+                if (!a.withhold)
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+                        "[%1], %2, [%3];" ::"r"(base + kOffPacked + s * kHalf),
+                        "l"(src), "r"(kHalf), "r"(bar_packed(s))
+                        : "memory");
                 ++e;
             };
             load(pages.key(), 0);

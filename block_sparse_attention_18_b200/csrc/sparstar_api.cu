@@ -502,13 +502,12 @@ SPARSTAR_API int64_t sparstar_kv4_attn_work_bytes(int64_t n, int64_t Hq, int64_t
     return sparstar::kv4_attn_work_bytes(s);
 }
 
-SPARSTAR_API int sparstar_kv4_attn(const sparstar_kv4_cache *cache, const void *q, int dtype,
-                                   int64_t n, int64_t Hq, int64_t Lq, const int32_t *seqs,
-                                   float tau, int causal, const int32_t *kv_idx,
-                                   const int32_t *kv_cnt, int64_t max_sel, void *out, float *lse,
-                                   void *work, int64_t work_bytes, int32_t *status,
-                                   void *stream) {
-    TraceRange trace("sparstar_kv4_attn");
+namespace {
+
+int kv4_attn(const sparstar_kv4_cache *cache, const void *q, int dtype, int64_t n, int64_t Hq,
+             int64_t Lq, const int32_t *seqs, float tau, int causal, const int32_t *kv_idx,
+             const int32_t *kv_cnt, int64_t max_sel, void *out, float *lse, void *work,
+             int64_t work_bytes, int32_t *status, void *stream, bool withhold) {
     sparstar::Kv4 c;
     if (!dtype_ok(dtype)) return SPARSTAR_EDTYPE;
     if (int rc = kv4_cache_check(cache, false, &c)) return rc;
@@ -530,9 +529,33 @@ SPARSTAR_API int sparstar_kv4_attn(const sparstar_kv4_cache *cache, const void *
     if (int rc = device_check()) return rc;
     const sparstar::Kv4Attn a{q,      (int32_t)n, (int32_t)Hq,      (int32_t)Lq, causal, seqs,
                               tau,    kv_idx,     kv_cnt,           (int32_t)max_sel,
-                              out,    lse,        work,             status};
+                              out,    lse,        work,             status,      withhold};
     return cuda_status(
         sparstar::launch_kv4_attn(c, a, s, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+SPARSTAR_API int sparstar_kv4_attn(const sparstar_kv4_cache *cache, const void *q, int dtype,
+                                   int64_t n, int64_t Hq, int64_t Lq, const int32_t *seqs,
+                                   float tau, int causal, const int32_t *kv_idx,
+                                   const int32_t *kv_cnt, int64_t max_sel, void *out, float *lse,
+                                   void *work, int64_t work_bytes, int32_t *status,
+                                   void *stream) {
+    TraceRange trace("sparstar_kv4_attn");
+    return kv4_attn(cache, q, dtype, n, Hq, Lq, seqs, tau, causal, kv_idx, kv_cnt, max_sel, out,
+                    lse, work, work_bytes, status, stream, false);
+}
+
+SPARSTAR_API int sparstar_test_kv4_attn_timeout(const sparstar_kv4_cache *cache, const void *q,
+                                                int dtype, int64_t n, int64_t Hq, int64_t Lq,
+                                                float tau, void *out, void *work,
+                                                int64_t work_bytes, int32_t *status,
+                                                void *stream) {
+    TraceRange trace("sparstar_test_kv4_attn_timeout");
+    if (!status) return SPARSTAR_EINVAL;
+    return kv4_attn(cache, q, dtype, n, Hq, Lq, nullptr, tau, 0, nullptr, nullptr, 0, out, nullptr,
+                    work, work_bytes, status, stream, true);
 }
 
 SPARSTAR_API int sparstar_test_attn_timeout(const void *q, const void *k, const void *v,

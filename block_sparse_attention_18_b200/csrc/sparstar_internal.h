@@ -125,6 +125,7 @@ struct Kv4Attn {
     float *lse;
     void *work;
     int32_t *status;
+    bool withhold = false;  // test hook: copies no page, so that the waits give up
 };
 // The sizes that decide which kernel takes a call and how much scratch.
 struct Kv4Shape {

@@ -81,6 +81,9 @@ def _load():
     L.sparstar_kv4_compact.argtypes = [kv4, vp, vp]
     L.sparstar_test_kv4_compact_timeout.argtypes = [kv4, vp, vp]
     L.sparstar_test_kv4_compact_timeout.restype = i32
+    L.sparstar_test_kv4_attn_timeout.argtypes = [kv4, vp, i32, i64, i64, i64, f32, vp, vp, i64, vp,
+                                                 vp]
+    L.sparstar_test_kv4_attn_timeout.restype = i32
     L.sparstar_kv4_write.argtypes = [kv4, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp]
     L.sparstar_kv4_read.argtypes = [kv4, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp]
     L.sparstar_kv4_attn.argtypes = [kv4, vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, i64, vp,
@@ -739,3 +742,15 @@ def sparstar_test_kv4_compact_timeout(cache: Kv4Cache, n_live):
     _check(lib.sparstar_test_kv4_compact_timeout(
         cache._struct, _kv4_tensor(cache, n_live, "n_live", torch.int32, (1,)),
         _kv4_raw_stream(cache)), "sparstar_test_kv4_compact_timeout")
+
+
+def sparstar_test_kv4_attn_timeout(cache: Kv4Cache, q, out, work, status):
+    """Test hook: attention of sequences 0..n-1 with its copies withheld, so
+    that its waits give up and STATUS_TIMEOUT is set in `status`.  ``work`` is
+    not to be used again."""
+    n, Hq, Lq, D = q.shape
+    _check(lib.sparstar_test_kv4_attn_timeout(
+        cache._struct, _kv4_tensor(cache, q, "q", q.dtype, q.shape), _DTYPE.get(q.dtype, -1), n,
+        Hq, Lq, _TAU[D], _kv4_tensor(cache, out, "out", q.dtype, q.shape), work.data_ptr(),
+        work.numel(), _kv4_status(cache, status), _kv4_raw_stream(cache)),
+        "sparstar_test_kv4_attn_timeout")

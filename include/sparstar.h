@@ -551,6 +551,17 @@ int sparstar_test_attn_timeout(const void *q, const void *k, const void *v, int6
 int sparstar_test_kv4_compact_timeout(const sparstar_kv4_cache *cache, int32_t *n_live,
                                       void *stream);
 
+/*
+ * sparstar_test_kv4_attn_timeout — TEST HOOK for failure detection:
+ * sparstar_kv4_attn with the copies of pages (or of the tiles unpacked from
+ * them) withheld.  Every role of the kernel gives up after about two seconds,
+ * waits as long for each copy that it asked for, and leaves; *status (required)
+ * gets SPARSTAR_STATUS_TIMEOUT, `out` and the zeros of `work` are undefined.
+ */
+int sparstar_test_kv4_attn_timeout(const sparstar_kv4_cache *cache, const void *q, int dtype,
+                                   int64_t n, int64_t Hq, int64_t Lq, float tau, void *out,
+                                   void *work, int64_t work_bytes, int32_t *status, void *stream);
+
 /* Message for a status code (static storage). */
 const char *sparstar_strerror(int code);
 

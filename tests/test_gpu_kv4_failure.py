@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from kv4_ref import BLOCK
-from test_gpu_kv4 import check_state, filled, ints, model, sp  # noqa: F401
+from test_gpu_kv4 import (BF16, F32, check_attn, check_state, filled, ints, model, new_status,
+                          queries, sp, status_of)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +38,26 @@ def test_nothing_to_copy_does_not_wait(sp):
     n_live = ints(7)
     sp.sparstar_test_kv4_compact_timeout(cache, n_live)
     assert int(n_live) == 2
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,Lq,width,dtype", [
+    ([900, 40], 4, 2, 1, None, BF16),       # few rows: a warp a part
+    ([900, 40], 4, 2, 1, 100, BF16),        # a pair of warps a tile
+    ([900, 40], 4, 2, 3, None, F32),
+    ([900, 40], 2, 2, 130, None, BF16),     # many rows, pages unpacked in place
+    ([900, 40, 2000, 0, 300], 8, 2, 150, None, BF16),  # many rows, pages unpacked first
+])
+def test_attention_whose_copies_give_up_says_so(sp, lens, Hq, Hkv, Lq, width, dtype):
+    cache = filled(sp, lens, Hkv, 128, max_pages=width)
+    q = queries(len(lens), Hq, Lq, 128, dtype)
+    need = sp.sparstar_kv4_attn_work_bytes(len(lens), Hq, Hkv, Lq, 128, cache.max_pages, dtype)
+    work = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    out, status = torch.zeros_like(q), new_status()
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    sp.sparstar_test_kv4_attn_timeout(cache, q, out, work, status)
+    assert status_of(status) == sp.STATUS_TIMEOUT
+    assert 1.0 < time.monotonic() - t0 < 60.0
+
+    # The same context goes on, with scratch of its own.
+    check_attn(sp, cache, q)

@@ -45,3 +45,18 @@ def test_a_stream_of_another_device_is_refused(sp):
                  lambda: sp.sparstar_kv4_attn(here, None, stream=there)):
         with pytest.raises(ValueError, match="stream"):
             call()
+
+
+def test_the_attention_hook_refuses_as_the_call_does(sp):
+    c = cache(sp)
+
+    def call(**kw):
+        f = dict(q=A, dtype=0, n=1, Hq=4, Lq=1, tau=0.1, out=A, work=A, bytes=1 << 40, status=A,
+                 stream=0)
+        f.update(kw)
+        return sp.lib.sparstar_test_kv4_attn_timeout(c, *f.values())
+    assert call(dtype=2) == sp.EDTYPE
+    for kw in (dict(q=0), dict(out=0), dict(work=0), dict(status=0), dict(status=MIS), dict(n=9),
+               dict(Hq=3), dict(Lq=0), dict(tau=float("inf"))):
+        assert call(**kw) == sp.EINVAL, kw
+    assert call(bytes=100) == sp.ESIZE
