@@ -33,12 +33,14 @@
 // multiplied term by term.
 //
 // Bounds.  The bytes of the pages at HBM's rate, in principle.  A page and head
-// costs a warp some 2,800 instructions, mostly on the integer pipe, of which
-// the twelve warps that the registers allow keep 58% busy: 18,064 pages and
-// heads (144,512 tokens, 16 heads, 315 MB) take 83 us, 3.8 TB/s, each further
-// one 3.4 ns, 5.1 TB/s.  At twice that length it takes 144 us, and the copies
-// alone 113; without the products or without the extraction of codes hardly
-// less, without the dequantisation's fma a sixth less.  A short line
+// costs a warp 2,500 instructions, half of them on the integer pipe.  With the
+// twelve warps that the registers allow, neither that pipe nor the issue slots
+// are above 55% busy: waits for the pipe, for results and for a slot come to
+// about equal shares.  18,064 pages and heads (144,512 tokens, 16 heads, 315 MB)
+// take 83 us, 3.8 TB/s, each further one 3.5 ns, 5.0 TB/s.  At twice that length
+// it takes 147 us, and the copies alone took 113 of then 144; without the
+// products or without the extraction of codes hardly less, without the
+// dequantisation's fma a sixth less.  A short line
 // is bound by the latencies in a row: 1 us to find the line, 1.5 the tiles, 1
 // the copy, 1.6 a page's arithmetic, 3 the joins; 897 tokens take 11.3 us.
 #include <cuda_bf16.h>
@@ -1016,10 +1018,12 @@ cudaError_t launch_kv4_attn_few(const Kv4 &c, const Kv4Attn &a, int dtype, cudaS
     p.ends = p.joins + (int64_t)2 * kCtas * R * (c.D + 2);
     // Eight rows: twelve warps, each with (halves of) pages of its own, keep the
     // registers that hide the latencies.  Where that gives some warps one half
-    // and some two or three, eight pairs of warps, each a page at a time, take
-    // less (16 heads: 6,000 tokens 14.1 us against 17.0, 9,000 tokens 15.7
-    // against 18.9; below, 1,000 tokens, 12.0 against 11.3, and above, 15,000
-    // tokens, 23.8 against 22.6).
+    // and some two or three, eight pairs of warps, a page each, take less (16
+    // heads: 3,000 tokens 12.2 us against 12.6, 6,000 tokens 14.0 against 18.2,
+    // 9,000 tokens 15.7 against 19.9; below, 1,000 tokens, 12.0 and 12.0, 2,000
+    // tokens 12.1 and 12.4; above, a pair would have more than one page).  The
+    // tables' widths decide, not the lengths, which only the device knows: 6,000
+    // tokens in a table of 258 pages take 18.3 us.
     const double most = (double)a.n * p.units * (lists ? a.max_sel : c.max_pages);
     // Not more than 8 * 148 tiles: no part of 8 * 148 has more than one.
     constexpr int kPairs = 8;

@@ -33,12 +33,17 @@
 // of its own joins the results, in order.
 //
 // Bounds.  Unpacked first: the tensor and the exponential units in turn, as in
-// attn_sm100.cu.  8,000 rows of 16 heads over 16,512 tokens, every block: 760
-// us, 1.42 PFLOP/s; over lists of 83 of the 129 blocks 555 us, 1.25 PFLOP/s, as
-// long as attn_sm100.cu takes over the values themselves; 28 us of each unpack
-// 135 MB (26 at HBM's rate).  In place: the unpacking warps, 1.43 us a page where
-// the MMAs of one block need 0.5: 128 rows over 72,000 tokens, 16 heads, 113 us.
+// attn_sm100.cu, and the power cap: 8,000 rows of 16 heads over 16,512 tokens,
+// every block, take 796 us on a cool GPU (1.36 PFLOP/s) and 909 in a run of such
+// calls; over lists of 83 of the 129 blocks 565 and 650 us, as attn_sm100.cu over
+// the values themselves (572 and 650); 28 us of each unpack 135 MB (26 at HBM's
+// rate).  In place: the unpacking warps, 1.43 us a page where the MMAs of one
+// block need 0.5: 128 rows over 72,000 tokens, 16 heads, 113 to 128 us.
 // Short calls: about 14 us of start, epilogue and joining beside the pages.
+//
+// How the work is cut follows the tables' widths wherever the device does not
+// choose (see chooses): 128 rows over 16,512 tokens, 16 heads, take 42 us in
+// tables of 129 pages, 63 of 258 and 207 of 1,200.
 #include "kv4.cuh"
 #include "sm100.cuh"
 

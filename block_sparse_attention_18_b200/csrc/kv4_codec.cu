@@ -307,8 +307,9 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t row = ((int64_t)sp.i * c.Hkv + sp.h) * tokens;
     const int first = sp.t0 - sp.shift, last = sp.t1 - sp.shift;
     // The values' words first: they are on their way while the keys pass.
-    const int w0 = first / 8, tiles = W * ((last + 7) / 8 - w0);  // at most a thread's two
+    const int w0 = first / 8, tiles = W * ((last + 7) / 8 - w0);
     constexpr int kTiles = (W * (kBlock / 8) + kThreads - 1) / kThreads;
+    static_assert(kTiles == 1, "eight words a thread, beside four of the keys");
     uint32_t r[kTiles][8];
     auto tile_of = [&](int i, int &cw, int &tw) {
         const int it = threadIdx.x + i * kThreads, n = (last + 7) / 8 - w0;

@@ -509,6 +509,9 @@ int sparstar_kv4_read(const sparstar_kv4_cache *cache, void *k, void *v, int dty
  *          before its first use; a call leaves them zero (unless it sets
  *          SPARSTAR_STATUS_TIMEOUT).  Calls that may overlap on the GPU need
  *          one each, graphs that may be replayed at the same time too.
+ * How the work is cut over the GPU follows max_pages where the device does not
+ * choose it from the lengths: tables several times wider than their sequences
+ * are served right, but more slowly.
  * A row that sees no token gets out = 0 and lse = -inf; so do all rows of a
  * slot outside the cache.  List entries outside the sequence's pages are
  * skipped; both set SPARSTAR_STATUS_BAD_INDEX.
